@@ -24,12 +24,14 @@ __all__ = [
     "IKEY_BYTES", "DIM", "HEADS", "indexer_workspace", "attention_workspace", "DecodeStack",
     "layer_pattern", "stage", "indexer_rescore", "topk_merge", "lse_merge", "ContextParallelLayer",
     "partition_entries", "all_gather_stacked", "indexer_topk_multi", "indexer_multi_workspace",
-    "hybrid_decode_attention_multi",
+    "hybrid_decode_attention_multi", "PagedCache", "kv_cache_append_paged", "kv_cache_read_paged",
+    "paged_decode_attention", "paged_window_attention", "paged_attention_workspace", "ENTRY_FP4_BYTES",
 ]
 
 DIM = 512
 DIM_NOPE = 448
 ENTRY_BYTES = 576
+ENTRY_FP4_BYTES = 368
 IKEY_BYTES = 32
 HEADS = 16
 IDX_HEADS = 4
@@ -50,6 +52,13 @@ class _Cache(C.Structure):
         ("iscales", C.c_void_p), ("win_kv", C.c_void_p), ("tail_kv", C.c_void_p),
         ("tail_gate", C.c_void_p), ("seq_len", C.c_void_p), ("pos_bias", C.c_void_p),
         ("w_idx", C.c_void_p),
+    ]
+
+
+class _Paged(C.Structure):
+    _fields_ = [
+        ("format", C.c_int32), ("page_size", C.c_int32), ("batch", C.c_int32), ("max_pages", C.c_int32),
+        ("n_pages", C.c_int64), ("pages", C.c_void_p), ("page_table", C.c_void_p), ("seq_len", C.c_void_p),
     ]
 
 
@@ -94,12 +103,20 @@ def _load():
     L.hybrid_decode_attention_multi.argtypes = [P, I, P, I64, I, P, I, P, I, I, P, I, I, F, P, P, P, S, P, P]
     L.csld_topk_merge.argtypes = [P, P, P, I, I, I, I64, I64, P, P]
     L.csld_lse_merge.argtypes = [P, P, I, I, I, P, P, P]
+    PG = C.POINTER(_Paged)
+    L.kv_cache_append_paged.argtypes = [PG, P, I64, I64, I, P, P, C.c_double, P, P]
+    L.kv_cache_read_paged.argtypes = [PG, P, I64, P, P, P]
+    L.csld_paged_attention_workspace_size.restype = S
+    L.csld_paged_attention_workspace_size.argtypes = []
+    L.paged_decode_attention.argtypes = [PG, P, I, I, F, P, I, P, P, S, P, P]
+    L.paged_window_attention.argtypes = [PG, P, I, I, I, I, F, P, I, P, P, S, P, P]
     for fn in ("csld_compress", "csld_compress_channel", "csld_compress_rope", "kv_cache_append_rope",
                "kv_cache_prefill_rope", "csld_compress_scaled", "kv_cache_append_scaled", "kv_cache_prefill_scaled",
                "hybrid_decode_attention_scaled", "csld_compress_perhead", "kv_cache_prefill_perhead",
                "kv_cache_append_perhead", "indexer_topk_perhead", "csa_compress", "hca_compress", "kv_cache_append", "kv_cache_prefill",
                "indexer_topk", "hybrid_decode_attention", "csld_stage", "indexer_rescore", "csld_topk_merge",
-               "csld_lse_merge", "indexer_topk_multi", "hybrid_decode_attention_multi"):
+               "csld_lse_merge", "indexer_topk_multi", "hybrid_decode_attention_multi", "kv_cache_append_paged",
+               "kv_cache_read_paged", "paged_decode_attention", "paged_window_attention"):
         getattr(L, fn).restype = I
     return L
 
@@ -513,6 +530,142 @@ def hybrid_decode_attention_multi(q, comp_kv, ratio, topk, win_kv, W, seq_len, s
                                              float(scale), _ptr(out), _ptr(lse), _ptr(ws), ws.numel(), _ptr(err),
                                              _stream()), "hybrid_decode_attention_multi")
     return out, lse
+
+
+# ---- paged entry cache --------------------------------------------------------------------
+class PagedCache:
+    """Raw tokens of B sequences as entries in pages (csld_paged_cache), in device memory owned by
+    torch: pages [n_pages, page_size * entry bytes] u8, page_table [B, max_pages] i32 (the page of
+    token t: page_table[b, t // page_size]), seq_len [B] i32; fmt "fp8" (576-byte entries) or "fp4"
+    (368 bytes per token).  The tensors are the caller's to fill and keep; page_table and seq_len may
+    be changed in place between calls, err collects the device flags."""
+
+    FORMATS = {"fp8": (8, ENTRY_BYTES), "fp4": (4, ENTRY_FP4_BYTES)}
+
+    def __init__(self, pages, page_table, seq_len, page_size, fmt="fp8", err=None):
+        if fmt not in self.FORMATS:
+            raise CsldError(f"fmt: expected one of {sorted(self.FORMATS)}, got {fmt!r}")
+        _need(pages, torch.uint8, "pages")
+        _need(page_table, torch.int32, "page_table")
+        _need(seq_len, torch.int32, "seq_len")
+        code, entry = self.FORMATS[fmt]
+        if page_table.dim() != 2 or seq_len.shape != page_table.shape[:1]:
+            raise CsldError(f"page_table {tuple(page_table.shape)} and seq_len {tuple(seq_len.shape)}: expected "
+                            "[B, max_pages] and [B]")
+        if pages.dim() < 2 or pages.numel() != pages.shape[0] * page_size * entry:
+            raise CsldError(f"pages {tuple(pages.shape)}: expected [n_pages, page_size * {entry}] bytes")
+        if not pages.device == page_table.device == seq_len.device:
+            raise CsldError("pages, page_table and seq_len lie on different devices")
+        self.fmt, self.page_size, self.entry_bytes = fmt, page_size, entry
+        self.pages, self.page_table, self.seq_len = pages, page_table, seq_len
+        self.batch, self.max_pages, self.n_pages = page_table.shape[0], page_table.shape[1], pages.shape[0]
+        self.device = pages.device
+        self.err = torch.zeros(1, dtype=torch.int32, device=self.device) if err is None else _need(err, torch.int32, "err")
+        self._struct = _Paged(code, page_size, self.batch, self.max_pages, self.n_pages, pages.data_ptr(),
+                              page_table.data_ptr(), seq_len.data_ptr())
+        self._ref = C.byref(self._struct)
+
+    @classmethod
+    def allocate(cls, batch, context, page_size=64, fmt="fp8", device="cuda"):
+        """An empty cache with room for `context` tokens of each sequence, its pages dealt out in order."""
+        per = -(-context // page_size)
+        dev = torch.device(device)
+        entry = cls.FORMATS[fmt][1] if fmt in cls.FORMATS else 0
+        return cls(torch.zeros((batch * per, page_size * entry), dtype=torch.uint8, device=dev),
+                   torch.arange(batch * per, dtype=torch.int32, device=dev).view(batch, per),
+                   torch.zeros(batch, dtype=torch.int32, device=dev), page_size, fmt)
+
+
+def _on_device(cache, what, *tensors):
+    """The call's tensors lie on the cache's device, and that device is the current one."""
+    if cache.device.index != torch.cuda.current_device():
+        raise CsldError(f"{what}: the cache is on {cache.device}, the current device is {torch.cuda.current_device()}")
+    for t in tensors:
+        if t is not None and t.device != cache.device:
+            raise CsldError(f"{what}: a tensor is on {t.device}, the cache on {cache.device}")
+
+
+def kv_cache_append_paged(cache: PagedCache, kv_new, n_new=None, start=None, rope_base=0.0, err=None):
+    """Append kv_new [B,T,512] bf16 (any strides that are multiples of 8, dims contiguous): the first
+    n_new[b] tokens of row b (all T without n_new) at positions start[b] (default seq_len[b]) on.
+    rope_base > 1 rotates dims 448..511 at each token's position; 0 stores them as given."""
+    if not kv_new.is_cuda or kv_new.dtype != torch.bfloat16 or kv_new.dim() != 3 or kv_new.shape[0] != cache.batch \
+            or kv_new.shape[2] != DIM or kv_new.stride(2) != 1:
+        raise CsldError(f"kv_new: expected a CUDA bfloat16 [{cache.batch}, T, {DIM}] tensor with contiguous rows, got "
+                        f"{kv_new.dtype} {tuple(kv_new.shape)} strides {kv_new.stride()} on {kv_new.device}")
+    for t, name in ((n_new, "n_new"), (start, "start")):
+        if t is not None and _need(t, torch.int32, name).shape != cache.seq_len.shape:
+            raise CsldError(f"{name}: expected shape {tuple(cache.seq_len.shape)}, got {tuple(t.shape)}")
+    err = cache.err if err is None else _need(err, torch.int32, "err")
+    _on_device(cache, "kv_cache_append_paged", kv_new, n_new, start, err)
+    T = kv_new.shape[1]
+    if T == 0:
+        raise CsldError("kv_new: no tokens")
+    # the stride of a dimension of length 1 is never used
+    _check(lib.kv_cache_append_paged(cache._ref, kv_new.data_ptr(), kv_new.stride(0) if cache.batch > 1 else 0,
+                                     kv_new.stride(1) if T > 1 else 0, T, _ptr(n_new), _ptr(start), rope_base,
+                                     err.data_ptr(), _stream()), "kv_cache_append_paged")
+
+
+def kv_cache_read_paged(cache: PagedCache, start, T, out=None, err=None):
+    """The bf16 values [B,T,512] of the entries at positions start[b] .. start[b]+T-1 (zeros outside
+    0 .. seq_len[b]-1)."""
+    if _need(start, torch.int32, "start").shape != cache.seq_len.shape:
+        raise CsldError(f"start: expected shape {tuple(cache.seq_len.shape)}, got {tuple(start.shape)}")
+    if out is None:
+        out = torch.empty((cache.batch, max(T, 0), DIM), dtype=torch.bfloat16, device=cache.device)
+    if _need(out, torch.bfloat16, "out").shape != (cache.batch, T, DIM):
+        raise CsldError(f"out: expected shape {(cache.batch, T, DIM)}, got {tuple(out.shape)}")
+    err = cache.err if err is None else _need(err, torch.int32, "err")
+    _on_device(cache, "kv_cache_read_paged", start, out, err)
+    _check(lib.kv_cache_read_paged(cache._ref, start.data_ptr(), T, out.data_ptr(), err.data_ptr(), _stream()),
+           "kv_cache_read_paged")
+    return out
+
+
+def paged_attention_workspace(device="cuda"):
+    """The workspace of paged_decode_attention / paged_window_attention, the same for every shape."""
+    with torch.cuda.device(torch.device(device)):
+        return torch.empty(lib.csld_paged_attention_workspace_size(), dtype=torch.uint8, device=device)
+
+
+def _paged_attention(what, call, cache, q, scale, out, lse, ws, err, *masks):
+    if not q.is_cuda or q.dtype != torch.bfloat16 or q.dim() != 4 or q.shape[0] != cache.batch or q.shape[3] != DIM \
+            or not q.is_contiguous():
+        raise CsldError(f"q: expected a contiguous CUDA bfloat16 [{cache.batch}, Q, heads, {DIM}] tensor, got {q.dtype} "
+                        f"{tuple(q.shape)} on {q.device}")
+    _, Q, heads, _ = q.shape
+    if out is None:
+        out = torch.empty_like(q)
+    elif out.dtype not in (torch.bfloat16, torch.float32) or out.shape != q.shape or not out.is_contiguous():
+        raise CsldError(f"out: expected a contiguous bfloat16 or float32 tensor of shape {tuple(q.shape)}, got "
+                        f"{out.dtype} {tuple(out.shape)}")
+    if lse is None:
+        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+    elif _need(lse, torch.float32, "lse").shape != q.shape[:3]:
+        raise CsldError(f"lse: expected shape {tuple(q.shape[:3])}, got {tuple(lse.shape)}")
+    if ws is None:
+        ws = paged_attention_workspace(q.device)
+    err = cache.err if err is None else _need(err, torch.int32, "err")
+    _on_device(cache, what, q, out, lse, ws, err)
+    _check(call(cache._ref, q.data_ptr(), heads, Q, *masks, scale, out.data_ptr(), int(out.dtype == torch.bfloat16),
+                lse.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), err.data_ptr(), _stream()), what)
+    return out, lse
+
+
+def paged_decode_attention(cache: PagedCache, q, scale, out=None, lse=None, ws=None, err=None):
+    """The Q newest tokens of each sequence over all tokens up to their own: q [B,Q,heads,512] bf16 ->
+    (out [B,Q,heads,512] bf16, or fp32 where such an `out` is given; lse [B,Q,heads] f32)."""
+    return _paged_attention("paged_decode_attention", lib.paged_decode_attention, cache, q, scale, out, lse, ws, err)
+
+
+def paged_window_attention(cache: PagedCache, q, W, sinks, scale, out=None, lse=None, ws=None, err=None):
+    """paged_decode_attention over a sliding window of the W newest tokens and the first `sinks` ones."""
+    for v, name in ((W, "W"), (sinks, "sinks")):
+        if not 0 <= v <= 0x7FFFFFFF:
+            raise CsldError(f"{name} {v} outside 0..2^31-1")
+    return _paged_attention("paged_window_attention", lib.paged_window_attention, cache, q, scale, out, lse, ws, err,
+                            W, sinks)
 
 
 # ---- staging copies -----------------------------------------------------------------------

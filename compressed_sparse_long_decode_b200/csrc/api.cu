@@ -9,6 +9,7 @@
 
 #include "csld_internal.cuh"
 #include "kernels.cuh"
+#include "paged.cuh"
 
 namespace csld {
 // stage.cu
@@ -518,6 +519,102 @@ csld_status csld_compress_channel(const uint16_t* raw, const float* gate, const 
                                                   num_sms(), as_stream(stream));
     if (e != cudaSuccess) return cuda_fail(e, "csld_compress_channel");
     return CSLD_OK;
+}
+
+namespace {
+csld_status check_paged(const csld_paged_cache* c, csld::PagedView* v) {
+    if (!c) return fail(CSLD_ERR_ARG, "cache is NULL");
+    if (c->format != CSLD_ENTRY_FP8 && c->format != CSLD_ENTRY_FP4)
+        return fail(CSLD_ERR_ARG, "format %d is neither CSLD_ENTRY_FP8 nor CSLD_ENTRY_FP4", c->format);
+    if (c->page_size < CSLD_PAGE_CHUNK || c->page_size > CSLD_PAGE_MAX || c->page_size % CSLD_PAGE_CHUNK)
+        return fail(CSLD_ERR_ARG, "page_size %d: need a multiple of %d in %d..%d", c->page_size, CSLD_PAGE_CHUNK,
+                    CSLD_PAGE_CHUNK, CSLD_PAGE_MAX);
+    if (c->batch < 1 || c->batch > 65535) return fail(CSLD_ERR_ARG, "batch %d outside 1..65535", c->batch);
+    if (c->max_pages < 1 || (int64_t)c->max_pages * c->page_size > (int64_t)INT32_MAX)
+        return fail(CSLD_ERR_ARG, "max_pages %d: need >= 1 and max_pages * page_size <= 2^31 - 1", c->max_pages);
+    if (c->n_pages < 1 || c->n_pages > (int64_t)INT32_MAX / c->page_size)
+        return fail(CSLD_ERR_ARG, "n_pages %lld: need >= 1 and n_pages * page_size <= 2^31 - 1", (long long)c->n_pages);
+    if (!c->pages || !c->page_table || !c->seq_len) return fail(CSLD_ERR_ARG, "a required cache pointer is NULL");
+    if (!aligned16(c->pages)) return fail(CSLD_ERR_ALIGN, "pages must be 16-byte aligned");
+    *v = csld::PagedView{c->pages, c->page_table, c->seq_len, c->n_pages, c->page_size, c->max_pages, c->batch};
+    return CSLD_OK;
+}
+
+csld_status paged_attention_impl(const char* name, const csld_paged_cache* cache, const uint16_t* q, int heads, int Q,
+                                 int W, int sinks, float scale, void* out, int out_type, float* lse_out, void* ws,
+                                 size_t ws_bytes, int32_t* err, void* stream) {
+    csld::PagedView v;
+    const csld_status s = check_paged(cache, &v);
+    if (s != CSLD_OK) return s;
+    if (heads < 1 || heads > CSLD_PAGED_MAX_HEADS)
+        return fail(CSLD_ERR_UNSUPPORTED, "heads %d outside 1..%d", heads, CSLD_PAGED_MAX_HEADS);
+    if (Q < 1 || Q > CSLD_MULTI_MAX_Q) return fail(CSLD_ERR_ARG, "Q %d outside 1..%d", Q, CSLD_MULTI_MAX_Q);
+    if (out_type != CSLD_OUT_F32 && out_type != CSLD_OUT_BF16) return fail(CSLD_ERR_ARG, "out_type %d unknown", out_type);
+    if (!(scale == scale) || scale == INFINITY || scale == -INFINITY) return fail(CSLD_ERR_ARG, "scale is not finite");
+    if (!q || !out) return fail(CSLD_ERR_ARG, "a required pointer is NULL");
+    if (!aligned16(q) || !aligned16(out)) return fail(CSLD_ERR_ALIGN, "q and out must be 16-byte aligned");
+    const size_t need = csld::paged_attention_ws_bytes(num_sms());
+    if (!ws || ws_bytes < need) return fail(CSLD_ERR_WORKSPACE, "workspace %zu bytes < required %zu", ws_bytes, need);
+    if (!aligned16(ws)) return fail(CSLD_ERR_ALIGN, "workspace must be 16-byte aligned");
+    cudaError_t e = csld::launch_paged_attention(v, cache->format == CSLD_ENTRY_FP4, q, heads, Q, W, sinks, scale, out,
+                                                 out_type == CSLD_OUT_BF16, lse_out, ws, num_sms(), err, as_stream(stream));
+    if (e != cudaSuccess) return cuda_fail(e, name);
+    return CSLD_OK;
+}
+}  // namespace
+
+csld_status kv_cache_append_paged(const csld_paged_cache* cache, const uint16_t* kv_new, int64_t seq_stride,
+                                  int64_t token_stride, int T, const int32_t* n_new, const int32_t* start,
+                                  double rope_base, int32_t* err, void* stream) {
+    csld::PagedView v;
+    const csld_status s = check_paged(cache, &v);
+    if (s != CSLD_OK) return s;
+    if (T < 1 || T > (1 << 20)) return fail(CSLD_ERR_ARG, "T %d outside 1..2^20", T);
+    if (rope_base != 0.0 && !(rope_base > 1.0 && rope_base <= 1e300))
+        return fail(CSLD_ERR_ARG, "rope_base %g: need 0 (no rotation) or a finite value above 1", rope_base);
+    if (!kv_new) return fail(CSLD_ERR_ARG, "a required pointer is NULL");
+    if (start == cache->seq_len) return fail(CSLD_ERR_ARG, "start must not be the cache's seq_len; pass NULL for it");
+    if (token_stride < CSLD_DIM && T > 1) return fail(CSLD_ERR_SHAPE, "token_stride %lld below %d", (long long)token_stride, CSLD_DIM);
+    if (seq_stride < 0 || token_stride < 0) return fail(CSLD_ERR_SHAPE, "a stride is negative");
+    if (!aligned16(kv_new) || (seq_stride & 7) || (token_stride & 7))
+        return fail(CSLD_ERR_ALIGN, "kv_new must be 16-byte aligned and its strides multiples of 8 elements");
+    cudaError_t e = csld::launch_append_paged(v, cache->format == CSLD_ENTRY_FP4, kv_new, seq_stride, token_stride, T,
+                                              n_new, start, rope_base, err, as_stream(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "kv_cache_append_paged");
+    return CSLD_OK;
+}
+
+csld_status kv_cache_read_paged(const csld_paged_cache* cache, const int32_t* start, int64_t T, uint16_t* out,
+                                int32_t* err, void* stream) {
+    csld::PagedView v;
+    const csld_status s = check_paged(cache, &v);
+    if (s != CSLD_OK) return s;
+    if (T < 1 || T > ((int64_t)1 << 30) || T * v.batch > ((int64_t)1 << 40))
+        return fail(CSLD_ERR_ARG, "T %lld outside 1..2^30, or batch * T above 2^40", (long long)T);
+    if (!start || !out) return fail(CSLD_ERR_ARG, "a required pointer is NULL");
+    if (!aligned16(out)) return fail(CSLD_ERR_ALIGN, "out must be 16-byte aligned");
+    cudaError_t e = csld::launch_read_paged(v, cache->format == CSLD_ENTRY_FP4, start, T, out, num_sms(), err,
+                                            as_stream(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "kv_cache_read_paged");
+    return CSLD_OK;
+}
+
+size_t csld_paged_attention_workspace_size(void) { return csld::paged_attention_ws_bytes(num_sms()); }
+
+csld_status paged_decode_attention(const csld_paged_cache* cache, const uint16_t* q, int heads, int Q, float scale,
+                                   void* out, int out_type, float* lse_out, void* ws, size_t ws_bytes, int32_t* err,
+                                   void* stream) {
+    return paged_attention_impl("paged_decode_attention", cache, q, heads, Q, 0, 0, scale, out, out_type, lse_out, ws,
+                                ws_bytes, err, stream);
+}
+
+csld_status paged_window_attention(const csld_paged_cache* cache, const uint16_t* q, int heads, int Q, int W, int sinks,
+                                   float scale, void* out, int out_type, float* lse_out, void* ws, size_t ws_bytes,
+                                   int32_t* err, void* stream) {
+    if (W < 1) return fail(CSLD_ERR_ARG, "W %d below 1", W);
+    if (sinks < 0) return fail(CSLD_ERR_ARG, "sinks %d below 0", sinks);
+    return paged_attention_impl("paged_window_attention", cache, q, heads, Q, W, sinks, scale, out, out_type, lse_out,
+                                ws, ws_bytes, err, stream);
 }
 
 }  // extern "C"

@@ -78,6 +78,7 @@ typedef enum csld_status {
 #define CSLD_DEVERR_BAD_INDEX 2u    /* hybrid_decode_attention: a top-k index was not visible */
 #define CSLD_DEVERR_SEQ_LEN 4u      /* a seq_len < 0; that sequence was treated as empty */
 #define CSLD_DEVERR_TIMEOUT 8u      /* a bounded wait for an asynchronous copy gave up */
+#define CSLD_DEVERR_PAGE 16u        /* a paged cache: a needed page-table entry was outside 0..n_pages-1 */
 
 CSLD_API int csld_abi_version(void);
 CSLD_API const char* csld_last_error(void);
@@ -371,6 +372,105 @@ CSLD_API csld_status hybrid_decode_attention_multi(const uint16_t* q, int heads,
                                                    const int32_t* seq_len, int B, int Q, float scale,
                                                    float* out, float* lse_out, void* ws,
                                                    size_t ws_bytes, int32_t* err, void* stream);
+
+/* ----------------------------------------------------------------------------------------
+ * Paged entry cache: raw tokens kept as entries in pages that any sequence may own, for the
+ * layers and blocks that attend to raw tokens (sliding-window layers, the multi-token-prediction
+ * block, short full-attention layers).  Where the ring of csld_layer_cache keeps the last W
+ * tokens of a sequence, pages keep any of them: a prefix shared by several sequences, the first
+ * tokens beside a sliding window, a whole context in 8 or 4 bits.
+ *   pages       [n_pages][page_size * entry bytes]  the entries, written by kv_cache_append_paged
+ *   page_table  [batch][max_pages]  page of token t of sequence b: page_table[b][t / page_size];
+ *               entries that no call needs may hold anything (-1 for a page given back)
+ *   seq_len     [batch]  tokens so far (int32, device)
+ * page_size: a multiple of 16, 16..1024; pages 16-byte aligned; n_pages * page_size and
+ * max_pages * page_size at most 2^31 - 1.  One page may appear in several rows (a shared prefix);
+ * appending into such a page is the caller's affair.
+ * Formats:
+ *   CSLD_ENTRY_FP8  576 B per token, the entry of the other caches (448 E4M3, scale 1, saturating;
+ *                   64 bf16), tokens of a page in order.
+ *   CSLD_ENTRY_FP4  368 B per token: the 448 dims in E2M1 with one power-of-two scale per 32 (the
+ *                   indexer keys' quantisation: the smallest sigma = 2^e with max|x| <= 6 sigma,
+ *                   -126 <= e <= 125; larger values saturate, a group that holds a NaN reads as
+ *                   NaN), the 64 RoPE dims in bf16.  Kept in chunks of 16 tokens, 5888 B each:
+ *     0..3583     [14 groups][16 tokens][16 B] codes; a little-endian 32-bit word holds 8 dims,
+ *                 dim i's magnitude index in bits 4i..4i+2, its sign in bit 8i + 7 (i < 4) or
+ *                 8(i - 4) + 3: a byte permute then turns half a word into four E4M3 bytes, and the
+ *                 signs drop in with one masked OR
+ *     3584..3807  [14 groups][16 tokens] e + 127 (255: a group with a NaN)
+ *     3808..3823  [16 tokens] the largest of the token's 14 bytes below 255; 3824..3839 zero
+ *     3840..5887  [16 tokens][64] bf16 RoPE dims
+ * -------------------------------------------------------------------------------------- */
+#define CSLD_ENTRY_FP8 8
+#define CSLD_ENTRY_FP4 4
+#define CSLD_ENTRY_FP4_BYTES 368
+#define CSLD_PAGE_CHUNK 16      /* tokens per chunk of the FP4 format; page_size is a multiple */
+#define CSLD_PAGE_MAX 1024
+#define CSLD_PAGED_MAX_HEADS 128
+
+typedef struct csld_paged_cache {
+    int32_t format;             /* CSLD_ENTRY_FP8 or CSLD_ENTRY_FP4 */
+    int32_t page_size;
+    int32_t batch;              /* 1..65535 */
+    int32_t max_pages;
+    int64_t n_pages;
+    uint8_t* pages;
+    const int32_t* page_table;
+    int32_t* seq_len;
+} csld_paged_cache;
+
+/* Append of up to T new tokens per sequence (decode: T = 1; draft tokens; a padded prefill chunk).
+ * Sequence b's tokens kv_new[b][0 .. n_b), n_b = n_new ? n_new[b] : T, become the entries at
+ * positions s_b .. s_b + n_b - 1, s_b = start ? start[b] : seq_len[b], and seq_len[b] = s_b + n_b.
+ * (start: where a sequence goes on, e.g. behind the draft tokens that were accepted; what lay at
+ * and past it is replaced or forgotten.  It must not be seq_len itself.)  rope_base > 1: dims
+ * 448..511 arrive before rotary encoding and are turned at the token's position (pairs and angles
+ * as in csld_compress_rope; angles reduced in double, the turn in fp32, one rounding to bf16);
+ * rope_base = 0: stored as given.  All of a sequence's tokens are stored or none: if one would pass
+ * max_pages * page_size, or needs a page outside 0..n_pages-1, or s_b or n_b is out of range, nothing
+ * of that sequence changes and CSLD_DEVERR_CAPACITY, _PAGE or _SEQ_LEN is ORed into *err.  Nothing
+ * but those entries is written.
+ *   kv_new: token i of sequence b at kv_new + b * seq_stride + i * token_stride (elements, multiples
+ *   of 8), 512 bf16 each, 16-byte aligned; n_new, start [batch] device int32 or NULL; 1 <= T <= 2^20. */
+CSLD_API csld_status kv_cache_append_paged(const csld_paged_cache* cache, const uint16_t* kv_new, int64_t seq_stride,
+                                           int64_t token_stride, int T, const int32_t* n_new, const int32_t* start,
+                                           double rope_base, int32_t* err, void* stream);
+
+/* The inverse: out[b][i] = the 512 bf16 values of the entry at position start[b] + i, i < T (exact:
+ * every stored value is a bf16 number).  Positions outside 0 .. seq_len[b]-1 give zeros; a page outside
+ * 0..n_pages-1 gives zeros and CSLD_DEVERR_PAGE.  out [batch][T][512] bf16, 16-byte aligned; start
+ * [batch] device int32; 1 <= T <= 2^30, batch * T <= 2^40. */
+CSLD_API csld_status kv_cache_read_paged(const csld_paged_cache* cache, const int32_t* start, int64_t T, uint16_t* out,
+                                         int32_t* err, void* stream);
+
+/* Attention of the Q newest tokens of each sequence over a paged cache.  Query j of sequence b stands
+ * at position p = seq_len[b] - Q + j and sees
+ *   paged_decode_attention  every token t <= p;
+ *   paged_window_attention  the tokens t <= p with t < sinks or t > p - W: a sliding window of the W
+ *                           newest and the first `sinks` tokens, which stay visible.
+ * Keys = values = the entries' 512 values: out[b][j][h] = softmax(scale q . K^T) V over them, one
+ * softmax; lse_out the natural log of its denominator in logit units.  A query that sees nothing
+ * (p < 0) gives out = 0 and lse = -inf.  Only pages that hold a visible token are read; where such a
+ * page is outside 0..n_pages-1 its tokens are left out and CSLD_DEVERR_PAGE is set.  What lies in
+ * masked places (behind a sequence's end, outside the window) may be anything, NaN included.
+ *   q [batch][Q][heads][512] bf16; out the same shape, fp32 (out_type CSLD_OUT_F32) or bf16
+ *   (CSLD_OUT_BF16); lse_out [batch][Q][heads] f32 or NULL; 1 <= heads <= CSLD_PAGED_MAX_HEADS,
+ *   1 <= Q <= CSLD_MULTI_MAX_Q, 1 <= W, 0 <= sinks; q, out, ws 16-byte aligned.
+ * Products: the bf16 query against the stored codes exactly, softmax weights as two E4M3 terms (about
+ * 2^-9) for the 8- and 4-bit dims and as bf16 for the RoPE dims; sums and statistics in fp32.  An fp4
+ * entry's group whose scale lies more than 2^14 below the entry's largest is rounded at 2^-9 of ... that
+ * span (its values are below 2^-14 of the entry's largest).
+ * Workspace: csld_paged_attention_workspace_size() bytes (the same for every shape), no initial
+ * contents needed; calls that share one must not overlap on the GPU. */
+#define CSLD_OUT_F32 0
+#define CSLD_OUT_BF16 1
+CSLD_API size_t csld_paged_attention_workspace_size(void);
+CSLD_API csld_status paged_decode_attention(const csld_paged_cache* cache, const uint16_t* q, int heads, int Q,
+                                            float scale, void* out, int out_type, float* lse_out, void* ws,
+                                            size_t ws_bytes, int32_t* err, void* stream);
+CSLD_API csld_status paged_window_attention(const csld_paged_cache* cache, const uint16_t* q, int heads, int Q, int W,
+                                            int sinks, float scale, void* out, int out_type, float* lse_out, void* ws,
+                                            size_t ws_bytes, int32_t* err, void* stream);
 
 /* ----------------------------------------------------------------------------------------
  * hybrid_decode_attention_static -- the same computation as hybrid_decode_attention, for

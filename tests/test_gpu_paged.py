@@ -1,0 +1,351 @@
+"""GPU parity of the paged entry cache: append (with and without rotation), read-back, sliding-window
+attention with first tokens kept, and full attention, over fp8 and fp4 entries, against the 64-bit
+reference of tests/paged_reference.py."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import synth
+from tests import paged_reference as R
+
+pytestmark = pytest.mark.gpu
+SCALE = 1.0 / math.sqrt(512.0)
+BASE = 10000.0
+
+
+@pytest.fixture(scope="module")
+def csld():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    import compressed_sparse_long_decode_b200 as m
+    return m
+
+
+def _tokens(g, *shape):
+    """bf16 tokens with magnitudes spread from token to token."""
+    x = torch.randn(*shape, 512, generator=g) * torch.exp(torch.randn(*shape, 1, generator=g))
+    return x.to(torch.bfloat16)
+
+
+class Pair:
+    """The same cache on the device (csld.PagedCache) and in numpy: lens tokens of each sequence already
+    stored (encoded by the reference), pages in random order, everything else in them garbage: 0xFF
+    bytes, which are NaNs in every part of both formats."""
+
+    def __init__(self, csld, lens, page, fmt, seed, extra=8, keep=None):
+        g = synth.gen(seed)
+        rng = np.random.default_rng(seed)
+        B = len(lens)
+        per = max(1, -(-(max(lens) + extra) // page))
+        n_pages = B * per + 3
+        table = rng.permutation(n_pages)[:B * per].reshape(B, per).astype(np.int32)
+        pages = np.full((n_pages, page * R.ENTRY[fmt]), 0xFF, np.uint8)
+        self.ref = R.Cache(pages, table, np.array(lens, np.int32), page, fmt)
+        for b, n in enumerate(lens):
+            x = _tokens(g, n).double().numpy() if n else np.zeros((0, 512))
+            for t in (range(n) if keep is None else [t for t in range(n) if keep(n, t)]):
+                self.ref.store(b, t, x[t])
+        if keep is not None:   # pages without a kept token are given back
+            for b, n in enumerate(lens):
+                for i in range(per):
+                    if not any(t < n and keep(n, t) for t in range(i * page, (i + 1) * page)):
+                        table[b, i] = -1 if i % 2 else n_pages + 5
+        self.dev = csld.PagedCache(torch.from_numpy(pages.copy()).cuda(), torch.from_numpy(table).cuda(),
+                                   torch.tensor(lens, dtype=torch.int32).cuda(), page, fmt)
+
+    def check_bytes(self, rope_ulp=0):
+        """Device pages equal the reference's; RoPE values within rope_ulp bf16 steps."""
+        torch.cuda.synchronize()
+        a, r = self.dev.pages.cpu().numpy(), self.ref.pages
+        assert np.array_equal(self.dev.seq_len.cpu().numpy(), self.ref.seq_len)
+        if rope_ulp == 0:
+            assert np.array_equal(a, r)
+            return
+        if self.ref.fmt == "fp8":
+            a, r = a.reshape(-1, 576), r.reshape(-1, 576)
+            cut = 448
+        else:
+            a, r = a.reshape(-1, 5888), r.reshape(-1, 5888)
+            cut = 3840
+        assert np.array_equal(a[:, :cut], r[:, :cut])
+        ab, rb = (x[:, cut:].copy().view(np.uint16) for x in (a, r))
+        av, rv = R.bf16_values(ab), R.bf16_values(rb)
+        same = ab == rb
+        # one bf16 step (2^-7 of the value), or the fp32 turn's own error where a pair cancels
+        with np.errstate(invalid="ignore"):
+            near = np.abs(av - rv) <= rope_ulp * 2.0 ** -7 * np.abs(rv) + 2.0 ** -20 * 64
+        assert np.all(same | near)
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+@pytest.mark.parametrize("lens,T,page,base,ragged,given", [
+    ([0], 1, 16, 0.0, False, False),
+    ([0, 15, 16, 17, 63], 1, 16, BASE, False, False),
+    ([5, 0, 40], 7, 48, BASE, True, True),
+    ([0, 3], 100, 32, 0.0, True, False),
+    ([1000, 3, 77], 33, 64, BASE, True, True),
+])
+def test_append_and_read_match_reference(csld, fmt, lens, T, page, base, ragged, given):
+    c = Pair(csld, lens, page, fmt, seed=len(lens) + T, extra=T + 8)
+    g = synth.gen(T)
+    B = len(lens)
+    x = _tokens(g, B, T)
+    x[0, 0, 5] = float("inf")
+    x[-1, -1, 40:72] = 0.0
+    n_new = torch.tensor([(i * T + T - 1) // max(1, B) if i else T for i in range(B)], dtype=torch.int32).clamp(max=T) if ragged else None
+    start = torch.tensor([max(0, n - 2) for n in lens], dtype=torch.int32) if given else None
+    wide = torch.randn(B, T, 3, 512, generator=g).to(torch.bfloat16).cuda()   # a strided view, as out of a fused projection
+    wide[:, :, 1] = x.cuda()
+    csld.kv_cache_append_paged(c.dev, wide[:, :, 1], n_new=None if n_new is None else n_new.cuda(),
+                               start=None if start is None else start.cuda(), rope_base=base)
+    c.ref.append(x.double().numpy(), None if n_new is None else n_new.numpy(), None if start is None else start.numpy(), base)
+    c.check_bytes(rope_ulp=1 if base else 0)
+    assert c.dev.err.item() == 0
+    back0 = torch.tensor([max(0, n - 3) for n in lens], dtype=torch.int32)
+    back = csld.kv_cache_read_paged(c.dev, back0.cuda(), T + 9).double().cpu().numpy()
+    dev = R.Cache(c.dev.pages.cpu().numpy(), c.ref.table, c.ref.seq_len, page, fmt)
+    for b in range(B):
+        for i in range(T + 9):
+            t = int(back0[b]) + i
+            want = dev.value(b, t) if t < c.ref.seq_len[b] else np.zeros(512)
+            assert np.array_equal(back[b, i], want), (b, t)
+
+
+def test_fp4_values_at_the_formats_edges(csld):
+    """Zero, smallest, largest, saturating, NaN groups and every rounding midpoint, bytes and values."""
+    c = Pair(csld, [0], 16, "fp4", seed=1)
+    x = torch.zeros(1, 6, 512)
+    x[0, 0, :32] = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0] * 4) * torch.tensor([1.0, -1.0] * 16)
+    x[0, 1, :448] = torch.logspace(-38, 38, 448)
+    x[0, 2, 0], x[0, 2, 33], x[0, 2, 64] = float("nan"), float("-inf"), 3.3e38
+    x[0, 3, :448] = 1e-40
+    x[0, 4, 100] = -0.0
+    x[0, 5, :448] = torch.tensor([1.0, 6.0, 6.03125, 3.0, 3.015625, 4.0, 2.0 ** -30] * 64)
+    x = x.to(torch.bfloat16)
+    csld.kv_cache_append_paged(c.dev, x.cuda())
+    v = x.double().numpy()
+    v[0, 2, 0] = 0.0    # the group is stored as NaN whatever its codes; compare those apart
+    c.ref.append(v, None, None, 0.0)
+    torch.cuda.synchronize()
+    a = c.dev.pages.cpu().numpy()[c.ref.table[0, 0]]
+    r = c.ref.pages[c.ref.table[0, 0]].copy()
+    assert a[3584 + 2] == 255
+    a = a.copy()
+    a[3584 + 2], a[2 * 16:3 * 16] = r[3584 + 2], r[2 * 16:3 * 16]
+    assert np.array_equal(a, r)
+    back = csld.kv_cache_read_paged(c.dev, torch.zeros(1, dtype=torch.int32).cuda(), 6).double().cpu().numpy()
+    assert np.isnan(back[0, 2, :32]).all() and not np.isnan(back[0, 2, 32:]).any()
+
+
+ATT = [
+    # lens, Q, H, page, W, sinks
+    ([1], 1, 16, 16, None, 0),
+    ([0, 1, 15, 16, 17], 1, 16, 16, None, 0),
+    ([95, 96, 97, 193], 1, 16, 48, None, 0),
+    ([700, 3], 2, 16, 64, None, 0),
+    ([333], 8, 5, 32, None, 0),
+    ([5, 0, 2], 8, 16, 16, None, 0),
+    ([260], 1, 128, 128, None, 0),
+    ([200, 150], 3, 24, 16, None, 0),
+    ([1500, 40, 700], 1, 16, 64, 128, 4),
+    ([300, 4, 0], 4, 16, 64, 128, 4),
+    ([120, 1], 1, 16, 16, 1, 0),
+    ([130], 4, 1, 16, 1, 1),
+    ([500], 1, 16, 32, 17, 33),
+    ([90], 2, 16, 16, 1000, 5),
+    ([100], 1, 16, 16, 5, 1000),
+    ([400, 399], 8, 32, 48, 64, 16),
+]
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+@pytest.mark.parametrize("lens,Q,H,page,W,sinks", ATT)
+def test_attention_matches_reference(csld, fmt, lens, Q, H, page, W, sinks):
+    keep = None
+    if W is not None:
+        keep = lambda n, t: t < sinks or t > n - Q - W   # noqa: E731
+    c = Pair(csld, lens, page, fmt, seed=sum(lens) + Q + H, keep=keep)
+    q = torch.randn(len(lens), Q, H, 512, generator=synth.gen(H)).to(torch.bfloat16)
+    ref = R.attention(c.ref, q.double().numpy(), SCALE, W, sinks)
+    for dt in (torch.bfloat16, torch.float32):
+        out = torch.full(q.shape, float("nan"), dtype=dt, device="cuda")
+        if W is None:
+            o, l = csld.paged_decode_attention(c.dev, q.cuda(), SCALE, out=out)
+        else:
+            o, l = csld.paged_window_attention(c.dev, q.cuda(), W, sinks, SCALE, out=out)
+        torch.cuda.synchronize()
+        assert c.dev.err.item() == 0
+        R.assert_attention(o, l, ref, f"{fmt} {lens} Q{Q} H{H} W{W} S{sinks} {dt}")
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+@pytest.mark.parametrize("scale", [8 * SCALE, -2 * SCALE, 0.0])
+def test_attention_with_peaked_flat_and_negative_scales(csld, fmt, scale):
+    c = Pair(csld, [1000, 37], 64, fmt, seed=9)
+    q = torch.randn(2, 1, 16, 512, generator=synth.gen(4)).to(torch.bfloat16)
+    o, l = csld.paged_decode_attention(c.dev, q.cuda(), scale)
+    R.assert_attention(o, l, R.attention(c.ref, q.double().numpy(), scale), f"{fmt} scale {scale}")
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+def test_rising_logits_move_the_running_maximum(csld, fmt):
+    """Token t's logit grows with t for half of the heads and falls for the others, by far more than any
+    lazily kept maximum allows, so every tile brings a new maximum."""
+    n = 1200
+    c = Pair(csld, [n], 64, fmt, seed=3)
+    d = torch.sign(torch.randn(512, generator=synth.gen(8)))
+    for t in range(n):
+        c.ref.store(0, t, (d * (t + 1) / 256.0).to(torch.bfloat16).double().numpy())
+    c.dev.pages.copy_(torch.from_numpy(c.ref.pages))
+    q = (d * torch.tensor([1.0, -1.0] * 8)[:, None])[None, None].to(torch.bfloat16).contiguous()
+    for scale in (SCALE, 4 * SCALE):
+        o, l = csld.paged_decode_attention(c.dev, q.cuda(), scale)
+        R.assert_attention(o, l, R.attention(c.ref, q.double().numpy(), scale), f"{fmt} rising {scale}")
+
+
+def test_fp4_entries_of_very_unlike_magnitudes(csld):
+    """Neighbouring tokens 2^40 apart, and groups of one token 2^20 apart."""
+    g = synth.gen(5)
+    c = Pair(csld, [200], 16, "fp4", seed=2)
+    for t in range(200):
+        x = torch.randn(512, generator=g) * 2.0 ** (-20 if t % 2 else 0)
+        if t % 3 == 0:
+            x[32:64] *= 2.0 ** -20
+        if t % 5 == 0:
+            x *= 2.0 ** -20
+        c.ref.store(0, t, x.to(torch.bfloat16).double().numpy())
+    c.dev.pages.copy_(torch.from_numpy(c.ref.pages))
+    q = torch.randn(1, 1, 16, 512, generator=g).to(torch.bfloat16)
+    ref = list(R.attention(c.ref, q.double().numpy(), SCALE))
+    # The kernel holds a group at most 2^14 below its entry's largest scale exactly, others rounded to
+    # 2^-16 of that scale, which is at most 1 here (max|x| < 6): 2^-16 on an output (A enters times
+    # 2^-8), and on a logit scale * 32 dims * max|q| (< 6) * 2^-16 < 2^-12.
+    ref[2] = ref[2] + 2.0 ** -8
+    ref[3] = ref[3] + 2.0 ** -12
+    o, l = csld.paged_decode_attention(c.dev, q.cuda(), SCALE)
+    R.assert_attention(o, l, ref, "unlike magnitudes")
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+def test_nan_and_infinite_values_reach_only_the_queries_that_see_them(csld, fmt):
+    c = Pair(csld, [64, 300], 16, fmt, seed=7)
+    x = torch.randn(512, generator=synth.gen(1)).double().numpy()
+    x[3] = np.nan
+    c.ref.store(1, 150, x)
+    c.dev.pages.copy_(torch.from_numpy(c.ref.pages))
+    q = torch.randn(2, 2, 16, 512, generator=synth.gen(2)).to(torch.bfloat16)
+    o, l = csld.paged_decode_attention(c.dev, q.cuda(), SCALE)
+    assert torch.isnan(o[1]).all() and torch.isnan(l[1]).all() and not torch.isnan(o[0]).any()
+    o, l = csld.paged_window_attention(c.dev, q.cuda(), 100, 4, SCALE)
+    R.assert_attention(o, l, R.attention(c.ref, q.double().numpy(), SCALE, 100, 4), fmt)
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+def test_shared_and_missing_pages(csld, fmt):
+    c = Pair(csld, [100, 100, 60], 16, fmt, seed=11)
+    c.ref.table[1, :4] = c.ref.table[0, :4]     # a shared prefix
+    c.ref.table[2, 1] = -1                      # tokens 16..31 of sequence 2 lost
+    c.ref.table[2, 2] = 10 ** 6
+    c.dev.page_table.copy_(torch.from_numpy(c.ref.table))
+    q = torch.randn(3, 1, 16, 512, generator=synth.gen(6)).to(torch.bfloat16)
+    o, l = csld.paged_decode_attention(c.dev, q.cuda(), SCALE)
+    R.assert_attention(o, l, R.attention(c.ref, q.double().numpy(), SCALE), fmt)
+    assert c.dev.err.item() == 16
+    c.dev.err.zero_()
+    back = csld.kv_cache_read_paged(c.dev, torch.tensor([0, 90, 10], dtype=torch.int32).cuda(), 12)
+    assert c.dev.err.item() == 16 and (back[2, 6:] == 0).all() and (back[1, 10:] == 0).all() and (back[2, :6] != 0).any()
+    # the append of a sequence that misses a page or room (112 tokens here) is refused as a whole, the
+    # others go through
+    before = c.dev.pages.clone()
+    x = _tokens(synth.gen(3), 3, 20)
+    for first, lens in ((100, [100, 100, 60]), (92, [112, 100, 60])):
+        c.dev.err.zero_()
+        start = torch.tensor([first, 10 ** 7, 30], dtype=torch.int32)
+        csld.kv_cache_append_paged(c.dev, x.cuda(), start=start.cuda())
+        c.ref.append(x.double().numpy(), None, start.numpy(), 0.0)
+        c.check_bytes()
+        assert c.dev.err.item() == (16 | 1) and list(c.ref.seq_len) == lens
+        assert torch.equal(before, c.dev.pages) == (first == 100)
+    c.dev.err.zero_()
+    csld.kv_cache_append_paged(c.dev, x.cuda(), n_new=torch.tensor([21, -1, 0], dtype=torch.int32).cuda())
+    torch.cuda.synchronize()
+    assert c.dev.err.item() == 4 and np.array_equal(c.dev.seq_len.cpu().numpy(), c.ref.seq_len)
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+def test_decode_run_append_window_and_full_together(csld, fmt):
+    """Prefill chunk, then decode steps with 2 draft tokens of which one is accepted: append, window
+    attention and full attention on the same cache, as a layer stack would use them; the last step
+    captured in a CUDA graph on a side stream and replayed."""
+    g = synth.gen(21)
+    B = 3
+    c = Pair(csld, [0, 0, 0], 32, fmt, seed=5, extra=200)
+    ws = csld.paged_attention_workspace()
+    pre, n0 = _tokens(g, B, 90), torch.tensor([90, 61, 7], dtype=torch.int32)
+    csld.kv_cache_append_paged(c.dev, pre.cuda(), n_new=n0.cuda(), rope_base=BASE)
+    c.ref.append(pre.double().numpy(), n0.numpy(), None, BASE)
+    x = torch.zeros(B, 2, 512, dtype=torch.bfloat16, device="cuda")
+    q = torch.zeros(B, 2, 16, 512, dtype=torch.bfloat16, device="cuda")
+    start = torch.zeros(B, dtype=torch.int32, device="cuda")
+    res = {}
+
+    def step():
+        csld.kv_cache_append_paged(c.dev, x, start=start, rope_base=BASE)
+        res["w"] = csld.paged_window_attention(c.dev, q, 32, 4, SCALE, ws=ws)
+        res["f"] = csld.paged_decode_attention(c.dev, q, SCALE, ws=ws)
+
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    for s in range(5):
+        hx, hq = _tokens(g, B, 2), torch.randn(B, 2, 16, 512, generator=g).to(torch.bfloat16)
+        at = n0 + s
+        x.copy_(hx)
+        q.copy_(hq)
+        start.copy_(at)
+        torch.cuda.synchronize()
+        if s < 3:
+            step()
+        else:
+            if s == 3:
+                with torch.cuda.graph(graph, stream=side):
+                    step()
+            graph.replay()
+        torch.cuda.synchronize()
+        c.ref.append(hx.double().numpy(), None, at.numpy(), BASE)
+        dev = R.Cache(c.dev.pages.cpu().numpy(), c.ref.table, c.ref.seq_len, 32, fmt)
+        c.check_bytes(rope_ulp=1)
+        R.assert_attention(*res["w"], R.attention(dev, hq.double().numpy(), SCALE, 32, 4), f"{fmt} window step {s}")
+        R.assert_attention(*res["f"], R.attention(dev, hq.double().numpy(), SCALE), f"{fmt} full step {s}")
+    assert c.dev.err.item() == 0
+
+
+def test_binding_refuses_bad_tensors(csld):
+    c = csld.PagedCache.allocate(2, 100, 16, "fp4")
+    q = torch.zeros(2, 1, 16, 512, dtype=torch.bfloat16, device="cuda")
+    x = torch.zeros(2, 1, 512, dtype=torch.bfloat16, device="cuda")
+    for call in (
+        lambda: csld.paged_decode_attention(c, q.float(), SCALE),
+        lambda: csld.paged_decode_attention(c, q[:1], SCALE),
+        lambda: csld.paged_decode_attention(c, q.cpu(), SCALE),
+        lambda: csld.paged_decode_attention(c, q, float("nan")),
+        lambda: csld.paged_decode_attention(c, q.expand(2, 9, 16, 512).contiguous(), SCALE),
+        lambda: csld.paged_decode_attention(c, q, SCALE, out=torch.zeros(2, 1, 16, 512, device="cuda", dtype=torch.float16)),
+        lambda: csld.paged_decode_attention(c, q, SCALE, ws=torch.zeros(64, dtype=torch.uint8, device="cuda")),
+        lambda: csld.paged_window_attention(c, q, 0, 4, SCALE),
+        lambda: csld.paged_window_attention(c, q, 1 << 32, 4, SCALE),
+        lambda: csld.paged_window_attention(c, q, 8, -1, SCALE),
+        lambda: csld.kv_cache_append_paged(c, x[:, :, :256]),
+        lambda: csld.kv_cache_append_paged(c, x.float()),
+        lambda: csld.kv_cache_append_paged(c, x, start=c.seq_len),
+        lambda: csld.kv_cache_append_paged(c, x, n_new=torch.ones(3, dtype=torch.int32, device="cuda")),
+        lambda: csld.kv_cache_append_paged(c, x, rope_base=0.5),
+        lambda: csld.kv_cache_read_paged(c, c.seq_len, 0),
+        lambda: csld.kv_cache_read_paged(c, c.seq_len, 4, out=torch.zeros(2, 4, 512, device="cuda")),
+        lambda: csld.PagedCache(c.pages, c.page_table, c.seq_len, 16, "fp8"),
+        lambda: csld.PagedCache(c.pages, c.page_table, c.seq_len, 16, "int4"),
+        lambda: csld.PagedCache(c.pages, c.page_table[0], c.seq_len, 16, "fp4"),
+    ):
+        with pytest.raises(csld.CsldError):
+            call()
+    torch.cuda.synchronize()
+    assert c.err.item() == 0 and c.seq_len.sum().item() == 0
