@@ -43,8 +43,8 @@ namespace csld {
 
 namespace {
 
-constexpr int kThreads = 768;
-constexpr int kConvWarp = 16, kConvWarps = 6, kCopyWarp = 22, kMmaWarp = 23;
+constexpr int kThreads = 960;
+constexpr int kConvWarp = 16, kConvWarps = 12, kCopyWarp = 28, kMmaWarp = 29;
 constexpr int kTile = 96;                        // entries per tile
 constexpr int kTileChunks = kTile / kChunk;      // 6
 constexpr int kBlkBytes = kTile * 128;           // one 128-byte column block of a tile
@@ -52,13 +52,18 @@ constexpr int kRopeBlk = 4;
 constexpr int kImgBytes = 5 * kBlkBytes;         // 60 KB
 constexpr int kStageBytes = kTileChunks * kChunk4Bytes;
 constexpr int kKBlocks = kTile / 32;
-constexpr float kRescaleLog2 = 8.f;
-// tensor-memory columns of stream s: S at kColS + 64 s (16 hi, 16 lo, 16 RoPE), O at kColO + 160 s (four dim blocks
-// of 32: hi, lo; RoPE 16)
-constexpr uint32_t kColS = 0, kColO = 128, kColOR = 128, kColSFA = 448, kColSFB = 456;
+// Weights: p = 2^(x - m), m the running maximum (fp8: less kLift8), kept until a logit lies more than kOver above it.
+// The PV operand holds p (fp4: p f_e g, g a power of two kept so that f_e g <= 2^7 when it is set and <= 2^10
+// later) in E5M2, whose 57344 bounds it: 2^5 * 2^10.
+constexpr float kLift8 = 10.f, kOver8 = 15.f, kOver4 = 5.f, kUnset = -1e30f;
+constexpr float kFeSet = 128.f, kFeMost = 1024.f;
+// tensor-memory columns of stream s: S at kColS + 48 s (16 hi, 16 lo, 16 RoPE), O at kColO + 208 s (four dim blocks
+// of 48: the three terms of P; RoPE 16)
+constexpr uint32_t kColS = 0, kStepS = 48, kColO = 96, kStepO = 208, kColOR = 192;
 constexpr uint32_t kIdQK = idesc_e4m3_m128(32, false, false);
 constexpr uint32_t kIdQKr = idesc_bf16_m128(16, false, false);
-constexpr uint32_t kIdPVr = idesc_bf16_m128(16, true, false);
+constexpr uint32_t kIdPV = idesc_e4m3_m128(48, true, true) | (1u << 10);   // B in E5M2
+constexpr uint32_t kIdPVr = idesc_bf16_m128(16, true, true);
 constexpr int kBarStream = 1, kBarAll = 3;       // named barriers: the streams' (1, 2), both streams' (3)
 constexpr int kLutNan = 19;                      // table row of a group that holds a NaN
 
@@ -69,22 +74,22 @@ struct Smem {
     uint8_t qk[4][32 * 128];                     // QK B operand per dim block: rows 0..15 Qhi, 16..31 Qlo (the MMAs also
                                                  // read past the last image into here: rows whose results go unused)
     uint8_t qr[16 * 128];                        // RoPE query
-    uint8_t p8[2][32 * 128];                     // per stream: PV B operand, rows 0..15 Phi, 16..31 Plo
-    uint8_t pbf[2][2][16 * 128];                 // per stream: bf16 P, two 64-entry K blocks
+    uint8_t p8[2][kTile * 64];                   // per stream: PV B operand [entry][16 heads x 3 terms], 64-byte swizzle
+    uint8_t pbf[2][kTile * 32];                  // per stream: bf16 P [entry][16 heads], 32-byte swizzle
     uint8_t stage[kFp4 ? 2 : 1][kFp4 ? kStageBytes : 16];
     uint2 lut[20];
-    float fe[kBufs][kTile];                      // entry factors; -1: masked
-    float c2[kHeads], sq[kHeads];
+    alignas(16) float fe[kBufs][kTile];          // entry factors; -1: masked (before the walk: the scan's sums)
+    alignas(16) float c2[kHeads];
     alignas(16) float tmax[2][4][kHeads];        // per stream: tile maxima (then partial sums) per lane quarter
-    alignas(16) uint8_t sfb[2][kHeads][4];       // per stream: P block scales [head][32-entry block]
+    float femax[2][4], ginv[2];                  // per stream: largest f_e per lane quarter; 1 / g
     float2 ml[2][kHeads];
     int32_t chunk_tok[kBufs][kTileChunks];       // first token of a tile's chunks; -1: none
     uint64_t stfull[kBufs], stempty[2], imgfull[kBufs], imgempty[kBufs], sfull[2], pfull[2], pdone[2], qready, drain;
-    int64_t red[24], prefix;
+    int64_t prefix;
     uint32_t tmem_base;
     int32_t fail, b0, n_issued;
 };
-static_assert(sizeof(Smem<true>) + 1024 <= 232448 && sizeof(Smem<false>) + 1024 <= 232448, "227 KB of shared memory");
+static_assert(sizeof(Smem<true>) <= 232448 && sizeof(Smem<false>) <= 232448, "227 KB of shared memory");
 
 struct Params {
     PagedView c;
@@ -194,59 +199,75 @@ __device__ __forceinline__ void decode8(uint32_t w, uint2 tab, uint32_t& lo, uin
 }
 
 // ---- softmax ----------------------------------------------------------------------------------
-// This thread's 8 logits (log2 units) of the tile whose S is in tensor memory.
+// t = x - m for this thread's 8 heads (log2 units; nm = -m), -inf where the entry is masked.
 template <bool kFp4>
-__device__ __forceinline__ void load_x(float (&x)[8], uint32_t ts, const float* c2, float fe, bool seen) {
-    uint32_t hi[8], lo[8];
+__device__ __forceinline__ void load_t(float (&t)[8], uint32_t ts, const float* c2, const float (&nm)[8], float fe, bool seen) {
+    uint32_t hi[8], lo[8], r[8];
     tmem_ld_32x32b_x8(ts, hi);
     tmem_ld_32x32b_x8(ts + 16u, lo);
-    if constexpr (kFp4) {
-        uint32_t r[8];
-        tmem_ld_32x32b_x8(ts + 32u, r);
-        tmem_ld_wait();
+    if constexpr (kFp4) tmem_ld_32x32b_x8(ts + 32u, r);
+    tmem_ld_wait();
+    const float4 ca = *reinterpret_cast<const float4*>(c2), cb = *reinterpret_cast<const float4*>(c2 + 4);
+    const float c[8] = {ca.x, ca.y, ca.z, ca.w, cb.x, cb.y, cb.z, cb.w};
 #pragma unroll
-        for (int h = 0; h < 8; ++h)
-            x[h] = seen ? fmaf(__uint_as_float(hi[h]) + __uint_as_float(lo[h]), fe, __uint_as_float(r[h])) * c2[h] : -INFINITY;
-    } else {
-        tmem_ld_wait();
-#pragma unroll
-        for (int h = 0; h < 8; ++h)
-            x[h] = seen ? (__uint_as_float(hi[h]) + __uint_as_float(lo[h])) * c2[h] : -INFINITY;
+    for (int h = 0; h < 8; ++h) {
+        float v = __uint_as_float(hi[h]) + __uint_as_float(lo[h]);
+        if constexpr (kFp4) v = fmaf(v, fe, __uint_as_float(r[h]));
+        t[h] = seen ? fmaf(v, c[h], nm[h]) : -INFINITY;
     }
 }
-// x <- p = 2^(x - m) (0 where the head has seen nothing yet), and p into the PV operands: p f_e as two E4M3 terms
-// after a power-of-two scale per 32 entries (a warp) and head, p as bf16 for the RoPE dims.
+__device__ __forceinline__ uint32_t f32x2_to_f16x2(float a, float b) {
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+// Two f16 -> two E5M2 bytes (round to nearest even).  E5M2 is f16's upper byte, so the way back is a byte permute.
+__device__ __forceinline__ uint32_t f16x2_to_e5m2x2(uint32_t v) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(v));
+    return r;
+}
+__device__ __forceinline__ uint32_t f16x2_sub(uint32_t a, uint32_t b) {
+    const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+// t <- p = 2^t, and p into the PV operands of this entry: p w (w = f_e g; fp8: p itself) as f16 and from there as
+// three E5M2 terms, each the rounding of what the ones before left (2^-3 of it: 2^-9 in all, and nothing finer
+// than E5M2's 2^-16, 2^-23 of the largest weight), 8 heads a store; p in bf16 for the RoPE dims.
 template <bool kFp4>
-__device__ __forceinline__ void write_p(uint8_t* p8, uint8_t* pb, uint8_t (*sfb)[4], const float (&m)[8], float (&x)[8],
-                                        float fe, int hg, int e, int sub, int lane) {
+__device__ __forceinline__ void write_p(uint8_t* p8, uint8_t* pb, float (&t)[8], float w, int hg, int e) {
+    uint32_t term[3][2], bf[4];
 #pragma unroll
-    for (int h = 0; h < 8; h += 2) {
-        const int hh = 8 * hg + h;
-        x[h] = m[h] == -INFINITY ? 0.f : exp2_ftz(x[h] - m[h]);
-        x[h + 1] = m[h + 1] == -INFINITY ? 0.f : exp2_ftz(x[h + 1] - m[h + 1]);
-        const float p0 = kFp4 ? x[h] * fe : x[h], p1 = kFp4 ? x[h + 1] * fe : x[h + 1];
-        const uint32_t pm0 = __reduce_max_sync(0xffffffffu, __float_as_uint(p0));   // p >= 0
-        const uint32_t pm1 = __reduce_max_sync(0xffffffffu, __float_as_uint(p1));
-        const int ks0 = pm0 >= 0x00800000u ? max(-126, min(127, 134 - static_cast<int>(pm0 >> 23))) : 0;
-        const int ks1 = pm1 >= 0x00800000u ? max(-126, min(127, 134 - static_cast<int>(pm1 >> 23))) : 0;
-        const float xs0 = p0 * pow2f(ks0), xs1 = p1 * pow2f(ks1);
-        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(xs0, xs1), __NV_SATFINITE, __NV_E4M3);
-        const uint32_t back = e4m3x2_to_f16x2(hi);   // exact
-        const float r0 = xs0 - __half2float(__ushort_as_half(static_cast<unsigned short>(back & 0xFFFFu)));
-        const float r1 = xs1 - __half2float(__ushort_as_half(static_cast<unsigned short>(back >> 16)));
-        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(r0, r1), __NV_SATFINITE, __NV_E4M3);
-        const uint32_t pbf2 = f32x2_to_bf16x2_bits(x[h], x[h + 1]);
-        if (e < kTile) {
-            p8[sw128(hh, e)] = static_cast<uint8_t>(hi);
-            p8[sw128(hh + 1, e)] = static_cast<uint8_t>(hi >> 8);
-            p8[sw128(16 + hh, e)] = static_cast<uint8_t>(lo);
-            p8[sw128(17 + hh, e)] = static_cast<uint8_t>(lo >> 8);
-            *reinterpret_cast<uint16_t*>(pb + sw128(hh, 2 * (e & 63))) = static_cast<uint16_t>(pbf2);
-            *reinterpret_cast<uint16_t*>(pb + sw128(hh + 1, 2 * (e & 63))) = static_cast<uint16_t>(pbf2 >> 16);
+    for (int h = 0; h < 8; h += 4) {
+        uint32_t v[2], q[3][2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int k = h + 2 * u;
+            t[k] = exp2_ftz(t[k]);
+            t[k + 1] = exp2_ftz(t[k + 1]);
+            bf[k >> 1] = f32x2_to_bf16x2_bits(t[k], t[k + 1]);
+            v[u] = kFp4 ? f32x2_to_f16x2(t[k] * w, t[k + 1] * w) : f32x2_to_f16x2(t[k], t[k + 1]);
+#pragma unroll
+            for (int n = 0; n < 3; ++n) {
+                q[n][u] = f16x2_to_e5m2x2(v[u]);
+                if (n < 2) v[u] = f16x2_sub(v[u], __byte_perm(q[n][u], 0u, 0x1404));   // exact
+            }
         }
-        if (lane == h) sfb[hh][sub] = static_cast<uint8_t>(127 - ks0);
-        if (lane == h + 1) sfb[hh + 1][sub] = static_cast<uint8_t>(127 - ks1);
+#pragma unroll
+        for (int n = 0; n < 3; ++n) term[n][h >> 2] = __byte_perm(q[n][0], q[n][1], 0x5410);
     }
+    const int sw = (e >> 1) & 3;
+#pragma unroll
+    for (int n = 0; n < 3; ++n)
+        *reinterpret_cast<uint2*>(p8 + 64 * e + 16 * (n ^ sw) + 8 * hg) = make_uint2(term[n][0], term[n][1]);
+    *reinterpret_cast<uint4*>(pb + 32 * e + 16 * (hg ^ ((e >> 2) & 1))) = make_uint4(bf[0], bf[1], bf[2], bf[3]);
+}
+// MN-major operand of rows of 64 or 32 bytes under the swizzle of that width: 8-row groups one after the other.
+__device__ __forceinline__ uint64_t desc_rows(const void* p, uint32_t row_bytes) {
+    uint64_t d = static_cast<uint64_t>((smem_u32(p) >> 4) & 0x3FFFu);
+    d |= static_cast<uint64_t>((8 * row_bytes) >> 4) << 32;
+    d |= static_cast<uint64_t>(1u) << 46;
+    d |= static_cast<uint64_t>(row_bytes == 64 ? 4u : 6u) << 61;
+    return d;
 }
 
 // The query of one head as MMA operands, one warp per head, 16 dims per lane: scaled by a power of two so that
@@ -261,10 +282,7 @@ __device__ __forceinline__ void prepare_query(Smem<kFp4>& sm, const uint4 (&v)[2
     top = __reduce_max_sync(0xffffffffu, top);
     const int sh = top ? max(-100, min(100, 7 - (static_cast<int>(top >> 7) - 127))) : 0;
     const float sq = pow2f(sh);
-    if (lane == 0) {
-        sm.sq[h] = sq;
-        sm.c2[h] = scale * 1.4426950408889634f / sq;
-    }
+    if (lane == 0) sm.c2[h] = scale * 1.4426950408889634f / sq;
     if (lane < kNope / 16) {
         uint32_t hw[4], lw[4];
 #pragma unroll
@@ -311,8 +329,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
                                                                       const __grid_constant__ Params P) {
     using S = Smem<kFp4>;
     constexpr int kBufs = S::kBufs;
-    extern __shared__ __align__(128) uint8_t smem_raw[];
-    S& sm = *reinterpret_cast<S*>(smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023));
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    S& sm = *reinterpret_cast<S*>(smem_raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
     // ---- setup --------------------------------------------------------------------------------
@@ -363,6 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
         mine += seq_info(P, b).tiles;
     }
     // tiles of all sequences, then (per batch of 768 sequences) the sequence that the share begins in
+    int64_t* red = reinterpret_cast<int64_t*>(sm.fe[0]);
     auto block_scan = [&](int64_t v, int64_t& total) {   // exclusive prefix of v over the threads
         int64_t inc = v;
 #pragma unroll
@@ -371,13 +390,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
             if (lane >= o) inc += y;
         }
         __syncthreads();
-        if (lane == 31) sm.red[warp] = inc;
+        if (lane == 31) red[warp] = inc;
         __syncthreads();
         int64_t before = 0;
         total = 0;
         for (int w = 0; w < kThreads / 32; ++w) {
-            if (w < warp) before += sm.red[w];
-            total += sm.red[w];
+            if (w < warp) before += red[w];
+            total += red[w];
         }
         return before + inc - v;
     };
@@ -419,11 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
             // ===== softmax: stream = warp / 8, thread = entry e (TMEM lane), heads 8 hg .. 8 hg + 7 ===============
             const int st = warp >> 3, hg = (warp >> 2) & 1, sub = warp & 3, e = 32 * sub + lane;
             const uint32_t lb = tmem + ((32u * sub) << 16);
-            const uint32_t ts = lb + kColS + 64u * st + 8u * hg, to = lb + kColO + 160u * st + 8u * hg;
-            if (warp < 4) {   // unit scale factors of V
-                tmem_st_32x32b_x8_fill(lb + kColSFA, 0x7F7F7F7Fu);
-                tmem_st_wait();
-            }
+            const uint32_t ts = lb + kColS + kStepS * st + 8u * hg, to = lb + kColO + kStepO * st + 8u * hg;
             auto load_query = [&](uint4 (&v)[2]) {
                 const int j = wk.rq / P.groups, h = 16 * (wk.rq % P.groups) + warp;
                 v[0] = v[1] = make_uint4(0, 0, 0, 0);
@@ -445,10 +460,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.qready);
                 named_barrier(kBarAll, 512);   // c2 of every head
-                float m[8], l[8];
+                float nm[8], l[8], g = 0.f;   // -m; g = 0: not set yet (fp4)
 #pragma unroll
                 for (int h = 0; h < 8; ++h) {
-                    m[h] = -INFINITY;
+                    nm[h] = -kUnset;
                     l[h] = 0.f;
                 }
                 const int T1 = T + wk.len;
@@ -458,63 +473,109 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
                     ok = ok && wait(&sm.sfull[st], (T >> 1) & 1, fail);
                     ok = __all_sync(0xffffffffu, ok);
                     tc_fence_after();
-                    float fe = ok && e < kTile ? sm.fe[buf][e] : -1.f;
-                    const bool seen = fe >= 0.f;
-                    fe = seen ? fe : 0.f;
+                    float t[8], fe = -1.f;
+                    bool over = false;
                     const float* c2 = sm.c2 + 8 * hg;
-                    float x[8];
-                    load_x<kFp4>(x, ts, c2, fe, seen);
                     // First try against the maximum as it stands (the common case): one meeting of the stream's
                     // warps.  S(T) complete implies PV(T-2) complete, so P and O are free to be written.
-                    bool over = false;
+                    if (sub < kTile / 32) {
+                        fe = ok ? sm.fe[buf][e] : -1.f;
+                        load_t<kFp4>(t, ts, c2, nm, fe, fe >= 0.f);
+                        float top = t[0];
 #pragma unroll
-                    for (int h = 0; h < 8; ++h) over |= x[h] > m[h] + kRescaleLog2;
-                    if (!__any_sync(0xffffffffu, over))
-                        write_p<kFp4>(sm.p8[st], sm.pbf[st][e >> 6], sm.sfb[st], m, x, fe, hg, e, sub, lane);
+                        for (int h = 1; h < 8; ++h) top = fmaxf(top, t[h]);
+                        over = top > (kFp4 ? kOver4 : kOver8) || (kFp4 && fe * g > kFeMost);
+                        if (!__any_sync(0xffffffffu, over)) write_p<kFp4>(sm.p8[st], sm.pbf[st], t, fe >= 0.f ? fe * g : 0.f, hg, e);
+                    }
                     fence_proxy_async_smem();
                     if (named_barrier_or(kBarStream + st, 256, over)) {
-                        load_x<kFp4>(x, ts, c2, fe, seen);
+                        const bool seen = fe >= 0.f;
+                        if (sub < kTile / 32) {
+                            load_t<kFp4>(t, ts, c2, nm, fe, seen);
 #pragma unroll
-                        for (int h = 0; h < 8; ++h) {
-                            const uint32_t km = __reduce_max_sync(0xffffffffu, score_key(x[h]));
-                            if (lane == h) sm.tmax[st][sub][8 * hg + h] = key_to_float(km);
+                            for (int h = 0; h < 8; ++h) {
+                                const uint32_t km = __reduce_max_sync(0xffffffffu, score_key(t[h]));
+                                if (lane == h) sm.tmax[st][sub][8 * hg + h] = key_to_float(km);
+                            }
+                            if (kFp4 && hg == 0) {
+                                const uint32_t fm = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(fe, 0.f)));
+                                if (lane == 0) sm.femax[st][sub] = __uint_as_float(fm);
+                            }
                         }
                         named_barrier(kBarStream + st, 256);
-                        float f[8];
+                        float f[8], fg = 1.f;
                         bool rescale = false;
+                        if constexpr (kFp4) {
+                            const float fm = fmaxf(fmaxf(sm.femax[st][0], sm.femax[st][1]), sm.femax[st][2]);
+                            if (fm > 0.f && (g == 0.f || fm * g > kFeMost)) {
+                                const float gn = kFeSet / fmaxf(fm, 0x1p-110f);
+                                if (g != 0.f) {
+                                    fg = gn / g;
+                                    rescale = true;
+                                }
+                                g = gn;
+                            }
+                        }
 #pragma unroll
                         for (int h = 0; h < 8; ++h) {
-                            float tm = sm.tmax[st][0][8 * hg + h];
+                            float tm = sm.tmax[st][0][8 * hg + h];   // relative to the old maximum
 #pragma unroll
-                            for (int q4 = 1; q4 < 4; ++q4) tm = fmaxf(tm, sm.tmax[st][q4][8 * hg + h]);
-                            const float mn = (tm > m[h] + kRescaleLog2 || m[h] == -INFINITY) ? fmaxf(tm, m[h]) : m[h];
-                            const bool up = mn != m[h] && m[h] != -INFINITY;
-                            f[h] = up ? exp2_ftz(m[h] - mn) : 1.f;
-                            rescale |= up;
+                            for (int q3 = 1; q3 < kTile / 32; ++q3) tm = fmaxf(tm, sm.tmax[st][q3][8 * hg + h]);
+                            const bool first = nm[h] == -kUnset, up = tm > (kFp4 ? kOver4 : kOver8);
+                            // a first maximum came out as x + 1e30, which lost x: it is formed below from S
+                            f[h] = up && !first ? exp2_ftz((kFp4 ? 0.f : kLift8) - tm) : 1.f;
+                            rescale |= up && !first;
                             l[h] *= f[h];
-                            m[h] = mn;
+                            if (up && !first) nm[h] -= tm - (kFp4 ? 0.f : kLift8);
+                        }
+                        bool unset = false;
+#pragma unroll
+                        for (int h = 0; h < 8; ++h) unset |= nm[h] == -kUnset;
+                        if (named_barrier_or(kBarStream + st, 256, unset)) {
+                            // some head has no maximum yet: the tile's own, from logits relative to zero
+                            float z[8];
+#pragma unroll
+                            for (int h = 0; h < 8; ++h) z[h] = 0.f;
+                            if (sub < kTile / 32) {
+                                load_t<kFp4>(t, ts, c2, z, fe, seen);
+#pragma unroll
+                                for (int h = 0; h < 8; ++h) {
+                                    const uint32_t km = __reduce_max_sync(0xffffffffu, score_key(t[h]));
+                                    if (lane == h) sm.tmax[st][sub][8 * hg + h] = key_to_float(km);
+                                }
+                            }
+                            named_barrier(kBarStream + st, 256);
+#pragma unroll
+                            for (int h = 0; h < 8; ++h) {
+                                float tm = sm.tmax[st][0][8 * hg + h];
+#pragma unroll
+                                for (int q3 = 1; q3 < kTile / 32; ++q3) tm = fmaxf(tm, sm.tmax[st][q3][8 * hg + h]);
+                                if (nm[h] == -kUnset && tm > -INFINITY) nm[h] = (kFp4 ? 0.f : kLift8) - tm;
+                            }
                         }
                         if (rescale) {   // the same answer in every thread of the head group
 #pragma unroll 1
-                            for (int c = 0; c < 9; ++c) {   // 4 blocks of (hi, lo), then RoPE
+                            for (int c = 0; c < 13; ++c) {   // 4 blocks of 3 terms, then RoPE
                                 uint32_t o[8];
+                                const float fc = c < 12 ? fg : 1.f;
                                 tmem_ld_32x32b_x8(to + 16u * c, o);
                                 tmem_ld_wait();
 #pragma unroll
-                                for (int h = 0; h < 8; ++h) o[h] = __float_as_uint(__uint_as_float(o[h]) * f[h]);
+                                for (int h = 0; h < 8; ++h) o[h] = __float_as_uint(__uint_as_float(o[h]) * (f[h] * fc));
                                 tmem_st_32x32b_x8(to + 16u * c, o);
                             }
                             tmem_st_wait();
                         }
-                        write_p<kFp4>(sm.p8[st], sm.pbf[st][e >> 6], sm.sfb[st], m, x, fe, hg, e, sub, lane);
+                        if (sub < kTile / 32) {
+                            load_t<kFp4>(t, ts, c2, nm, fe, seen);
+                            write_p<kFp4>(sm.p8[st], sm.pbf[st], t, seen ? fe * g : 0.f, hg, e);
+                        }
                         fence_proxy_async_smem();
                         named_barrier(kBarStream + st, 256);
                     }
+                    if (sub < kTile / 32) {
 #pragma unroll
-                    for (int h = 0; h < 8; ++h) l[h] += x[h];
-                    if (hg == 0) {   // block-scale word of operand row `lane` (rows h and 16 + h: head lane % 16)
-                        tmem_st_32x32b_x1(lb + kColSFB + 4u * st, *reinterpret_cast<const uint32_t*>(sm.sfb[st][lane & 15]));
-                        tmem_st_wait();
+                        for (int h = 0; h < 8; ++h) l[h] += t[h];
                     }
                     tc_fence_before();
                     __syncwarp();
@@ -534,10 +595,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
                 named_barrier(kBarStream + st, 256);
                 if (sub == 0 && lane < 8) {
                     const int hh = 8 * hg + lane;
-                    float mm = m[0];
+                    float mm = nm[0];
 #pragma unroll
-                    for (int h = 1; h < 8; ++h) mm = lane == h ? m[h] : mm;
-                    sm.ml[st][hh] = make_float2(mm, (sm.tmax[st][0][hh] + sm.tmax[st][1][hh]) + (sm.tmax[st][2][hh] + sm.tmax[st][3][hh]));
+                    for (int h = 1; h < 8; ++h) mm = lane == h ? nm[h] : mm;
+                    if (hh == 0) sm.ginv[st] = g != 0.f ? 1.f / g : 1.f;
+                    sm.ml[st][hh] = make_float2(-mm, (sm.tmax[st][0][hh] + sm.tmax[st][1][hh]) + (sm.tmax[st][2][hh] + sm.tmax[st][3][hh]));
                 }
                 tc_fence_before();
                 named_barrier(kBarAll, 512);
@@ -566,6 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
 #pragma unroll
                     for (int h = 0; h < 8; ++h) inv[h] = whole ? (L[h] == 0.f ? 0.f : 1.f / L[h]) : 1.f;
                     const uint32_t o0 = lb + kColO + 8u * hg;
+                    const float gi[2] = {sm.ginv[0], sm.ginv[1]};
 #pragma unroll 1
                     for (int c = 2 * st; c < 2 + 3 * st; ++c) {
                         const bool rope = c == 4;
@@ -575,15 +638,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
                             if (!(k ? use1 : use0)) continue;   // uniform in the warp
-                            uint32_t oh[8], ol[8];
-                            tmem_ld_32x32b_x8(o0 + 160u * k + 32u * c, oh);
-                            if (!rope) tmem_ld_32x32b_x8(o0 + 160u * k + 32u * c + 16u, ol);
-                            tmem_ld_wait();
+#pragma unroll 1
+                            for (int n = 0; n < (rope ? 1 : 3); ++n) {
+                                uint32_t o[8];
+                                tmem_ld_32x32b_x8(o0 + kStepO * k + 48u * c + 16u * n, o);
+                                tmem_ld_wait();
 #pragma unroll
-                            for (int h = 0; h < 8; ++h) {
-                                const float a = k ? a1[h] : a0[h];
-                                const float o = rope ? __uint_as_float(oh[h]) : __uint_as_float(oh[h]) + __uint_as_float(ol[h]);
-                                if (a != 0.f) v[h] = fmaf(a, o, v[h]);
+                                for (int h = 0; h < 8; ++h) {
+                                    const float a = (k ? a1[h] : a0[h]) * (rope ? 1.f : gi[k]);
+                                    if (a != 0.f) v[h] = fmaf(a, __uint_as_float(o[h]), v[h]);
+                                }
                             }
                         }
                         const int d = rope ? kNope + e : 128 * c + e;
@@ -624,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
             }
         } else if (warp < kConvWarp + kConvWarps) {
             // ===== convert ==================================================================================
-            const int ct = tid - 32 * kConvWarp, e = ct % kTile, half = ct / kTile;
+            const int ct = tid - 32 * kConvWarp, e = ct % kTile, part = ct / kTile;   // part: groups part, part + 4, ..
             int T = 0;
             for (; wk.left > 0; wk.next(P)) {
                 const int p = wk.s.n - P.Q + wk.rq / P.groups;   // the query's position
@@ -643,10 +707,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
                     if constexpr (kFp4) {
                         const uint8_t* ch = sm.stage[buf] + ck * kChunk4Bytes;
                         const uint32_t base = ch[kChunk4Exp + kGroups * kChunk + tk];
-                        if (half == 0) sm.fe[buf][e] = vis ? ldexpf(1.f, static_cast<int>(base) - 133) : -1.f;
+                        if (part == 0) sm.fe[buf][e] = vis ? ldexpf(1.f, static_cast<int>(base) - 133) : -1.f;
 #pragma unroll
-                        for (int i = 0; i < kGroups / 2; ++i) {
-                            const int g = half * (kGroups / 2) + i;
+                        for (int i = 0; i < 4; ++i) {
+                            const int g = part + 4 * i;
+                            if (g >= kGroups) break;   // whole warps
                             uint4 w = *reinterpret_cast<const uint4*>(ch + g * 256 + tk * 16);
                             const uint32_t ex = ch[kChunk4Exp + g * kChunk + tk];
                             if (!vis) w = make_uint4(0, 0, 0, 0);
@@ -656,22 +721,22 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
                             decode8(w.y, tab, a.z, a.w);
                             decode8(w.z, tab, b.x, b.y);
                             decode8(w.w, tab, b.z, b.w);
-                            uint8_t* dst = img + (g >> 2) * kBlkBytes;
-                            *reinterpret_cast<uint4*>(dst + sw128(e, 32 * (g & 3))) = a;
-                            *reinterpret_cast<uint4*>(dst + sw128(e, 32 * (g & 3) + 16)) = b;
+                            uint8_t* dst = img + i * kBlkBytes;
+                            *reinterpret_cast<uint4*>(dst + sw128(e, 32 * part)) = a;
+                            *reinterpret_cast<uint4*>(dst + sw128(e, 32 * part + 16)) = b;
                         }
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {   // RoPE rows, eight threads per entry (no bank conflicts)
-                            const int en = (ct >> 3) + 24 * i, c = ct & 7;
+                        for (int i = 0; i < 2; ++i) {   // RoPE rows, eight threads per entry (no bank conflicts)
+                            const int en = (ct >> 3) + 48 * i, c = ct & 7;
                             uint4 w = *reinterpret_cast<const uint4*>(sm.stage[buf] + (en / kChunk) * kChunk4Bytes + kChunk4Rope +
                                                                       (en % kChunk) * 2 * kRope + 16 * c);
                             if (!(ok && seen(en))) w = make_uint4(0, 0, 0, 0);
                             *reinterpret_cast<uint4*>(img + kRopeBlk * kBlkBytes + sw128(en, 16 * c)) = w;
                         }
                     } else {
-                        if (half == 0) sm.fe[buf][e] = vis ? 1.f : -1.f;
+                        if (part == 0) sm.fe[buf][e] = vis ? 1.f : -1.f;
                         if (!vis && ok) {
-                            for (int c = half; c < 40; c += 2)
+                            for (int c = part; c < 40; c += 4)
                                 *reinterpret_cast<uint4*>(img + (c >> 3) * kBlkBytes + sw128(e, 16 * (c & 7))) = make_uint4(0, 0, 0, 0);
                         }
                     }
@@ -739,20 +804,19 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
                     const int st = np & 1, buf = np % kBufs;
                     tc_fence_after();
                     const uint32_t acc0 = pt >= 2 ? 1u : 0u;   // the stream's first tile of the segment overwrites O
-                    const uint64_t da = desc_sw128(sm.img[buf], 0), dp = desc_sw128(sm.p8[st], 0);
-                    const uint32_t o = tmem + kColO + 160u * st, sfb = tmem + kColSFB + 4u * st;
+                    const uint64_t da = desc_sw128(sm.img[buf], 0), dp = desc_rows(sm.p8[st], 64);
+                    const uint32_t o = tmem + kColO + kStepO * st;
 #pragma unroll
                     for (int mb = 0; mb < 4; ++mb)
 #pragma unroll
                         for (int kb = 0; kb < kKBlocks; ++kb)
-                            umma_mxf8f6f4(o + 32u * mb, da + (mb * kBlkBytes + kb * 4096) / 16, dp + (32 * kb) / 16,
-                                          idesc_mxe4m3_m128(32, true, false, kb), tmem + kColSFA,
-                                          sfb | (static_cast<uint32_t>(kb) << 30), kb > 0 ? 1u : acc0);
+                            umma_f8f6f4(o + 48u * mb, da + (mb * kBlkBytes + kb * 4096) / 16, dp + (32 * 64 * kb) / 16, kIdPV,
+                                        kb > 0 ? 1u : acc0);
                     const uint64_t dar = desc_sw128(sm.img[buf] + kRopeBlk * kBlkBytes, kBlkBytes);
-                    const uint64_t dpb = desc_sw128(sm.pbf[st][0], 0);
+                    const uint64_t dpb = desc_rows(sm.pbf[st], 32);
 #pragma unroll
                     for (int ks = 0; ks < kTile / 16; ++ks)
-                        umma_f16(o + kColOR, dar + (ks * 2048) / 16, dpb + ((ks >> 2) * 2048 + 32 * (ks & 3)) / 16, kIdPVr,
+                        umma_f16(o + kColOR, dar + (ks * 2048) / 16, dpb + (16 * 32 * ks) / 16, kIdPVr,
                                  ks > 0 ? 1u : acc0);
                     umma_commit(&sm.imgempty[buf]);
                     umma_commit(&sm.pdone[st]);
@@ -768,7 +832,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
                     (qt > 0 || mbar_test(&sm.qready, seg & 1))) {
                     const int st = nq & 1;
                     tc_fence_after();
-                    const uint32_t d = tmem + kColS + 64u * st;
+                    const uint32_t d = tmem + kColS + kStepS * st;
                     const uint64_t da = desc_sw128(sm.img[nq % kBufs], 0);
 #pragma unroll
                     for (int kb = 0; kb < 4; ++kb)
@@ -934,7 +998,7 @@ cudaError_t launch_paged_attention(const PagedView& c, bool fp4, const uint16_t*
     CUtensorMap map = {};   // fp8: the pages as rows of 576 bytes
     if (!fp4 && !make_tensor_map_2d_u8(&map, c.pages, kEntry, (uint64_t)c.n_pages * c.page_size, 128, kChunk))
         return cudaErrorInvalidValue;
-    const size_t smem = (fp4 ? sizeof(Smem<true>) : sizeof(Smem<false>)) + 1024;
+    const size_t smem = fp4 ? sizeof(Smem<true>) : sizeof(Smem<false>);
     auto kernel = fp4 ? paged_attention_kernel<true> : paged_attention_kernel<false>;
     cudaError_t e = set_smem_once(kernel, smem);
     if (e != cudaSuccess) return e;
