@@ -52,11 +52,12 @@ constexpr int kRopeBlk = 4;
 constexpr int kImgBytes = 5 * kBlkBytes;         // 60 KB
 constexpr int kStageBytes = kTileChunks * kChunk4Bytes;
 constexpr int kKBlocks = kTile / 32;
-// Weights: p = 2^(x - m), m the running maximum (fp8: less kLift8), kept until a logit lies more than kOver above it.
-// The PV operand holds p (fp4: p f_e g, g a power of two kept so that f_e g <= 2^7 when it is set and <= 2^10
-// later) in E5M2, whose 57344 bounds it: 2^5 * 2^10.
-constexpr float kLift8 = 10.f, kOver8 = 15.f, kOver4 = 5.f, kUnset = -1e30f;
-constexpr float kFeSet = 128.f, kFeMost = 1024.f;
+// Weights: p = 2^(x + nm); a head's nm is set so that the largest p of a tile is 2^kLift and kept until one exceeds
+// 2^kOver.  The PV operand holds p w in E5M2, w = 1 (fp8) or f_e g (fp4; g a power of two set so that the tile's
+// largest f_e g is kFeSet, kept until one exceeds kFeMost).  E5M2 bounds the product: 57344 > 2^kOver w.
+template <bool kFp4> constexpr float kLift = kFp4 ? 0.f : 5.f;
+template <bool kFp4> constexpr float kOver = kFp4 ? 10.f : 15.f;
+constexpr float kFeSet = 8.f, kFeMost = 32.f, kUnset = 1e30f;
 // tensor-memory columns of stream s: S at kColS + 48 s (16 hi, 16 lo, 16 RoPE), O at kColO + 208 s (four dim blocks
 // of 48: the three terms of P; RoPE 16)
 constexpr uint32_t kColS = 0, kStepS = 48, kColO = 96, kStepO = 208, kColOR = 192;
@@ -65,7 +66,7 @@ constexpr uint32_t kIdQKr = idesc_bf16_m128(16, false, false);
 constexpr uint32_t kIdPV = idesc_e4m3_m128(48, true, true) | (1u << 10);   // B in E5M2
 constexpr uint32_t kIdPVr = idesc_bf16_m128(16, true, true);
 constexpr int kBarStream = 1, kBarAll = 3;       // named barriers: the streams' (1, 2), both streams' (3)
-constexpr int kLutNan = 19;                      // table row of a group that holds a NaN
+constexpr int kLutRows = 21;                     // NaN group; j = 0..18; all zero (j >= 19, masked entries)
 
 template <bool kFp4>
 struct Smem {
@@ -77,7 +78,7 @@ struct Smem {
     uint8_t p8[2][kTile * 64];                   // per stream: PV B operand [entry][16 heads x 3 terms], 64-byte swizzle
     uint8_t pbf[2][kTile * 32];                  // per stream: bf16 P [entry][16 heads], 32-byte swizzle
     uint8_t stage[kFp4 ? 2 : 1][kFp4 ? kStageBytes : 16];
-    uint2 lut[20];
+    uint2 lut[kLutRows];
     alignas(16) float fe[kBufs][kTile];          // entry factors; -1: masked (before the walk: the scan's sums)
     alignas(16) float c2[kHeads];
     alignas(16) float tmax[2][4][kHeads];        // per stream: tile maxima (then partial sums) per lane quarter
@@ -322,6 +323,69 @@ __device__ __forceinline__ void store_out(const Params& P, int64_t at, float v) 
     else reinterpret_cast<float*>(P.out)[at] = v;
 }
 
+// The MMAs of one tile.  Stream and image are compile-time constants and tensor memory starts at column 0 (all of it
+// is allocated), so descriptors are constants over one base: forming them at run time cost the issuing thread about
+// 95 cycles an MMA, twice what the tensor pipe takes for these narrow ones (45).
+template <bool kFp4, int kSt, int kBuf>
+__device__ __forceinline__ void issue_qk(Smem<kFp4>& sm) {
+    const uint64_t da = desc_sw128(sm.img[kBuf], 0), dq = desc_sw128(sm.qk[0], 0), dqr = desc_sw128(sm.qr, 0);
+    constexpr uint32_t d = kColS + kStepS * kSt;
+#pragma unroll
+    for (int kb = 0; kb < 4; ++kb)
+#pragma unroll
+        for (int ks = 0; ks < (kb < 3 ? 4 : 2); ++ks)
+            umma_f8f6f4(d, da + (kb * kBlkBytes + 32 * ks) / 16, dq + (kb * 4096 + 32 * ks) / 16, kIdQK, (kb | ks) != 0 ? 1u : 0u);
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks)   // fp4: apart, since f_e multiplies only the 4-bit dims
+        umma_f16(d + (kFp4 ? 32u : 0u), da + (kRopeBlk * kBlkBytes + 32 * ks) / 16, dqr + (32 * ks) / 16, kIdQKr,
+                 kFp4 && ks == 0 ? 0u : 1u);
+    umma_commit(&sm.sfull[kSt]);
+}
+template <bool kFp4, int kSt, int kBuf>
+__device__ __forceinline__ void issue_pv(Smem<kFp4>& sm, uint32_t acc0) {   // acc0 = 0: O is overwritten
+    const uint64_t da = desc_sw128(sm.img[kBuf], 0), dp = desc_rows(sm.p8[kSt], 64);
+    constexpr uint32_t o = kColO + kStepO * kSt;
+#pragma unroll
+    for (int mb = 0; mb < 4; ++mb)
+#pragma unroll
+        for (int kb = 0; kb < kKBlocks; ++kb)
+            umma_f8f6f4(o + 48u * mb, da + (mb * kBlkBytes + kb * 4096) / 16, dp + (32 * 64 * kb) / 16, kIdPV, kb > 0 ? 1u : acc0);
+    const uint64_t dar = desc_sw128(sm.img[kBuf] + kRopeBlk * kBlkBytes, kBlkBytes), dpb = desc_rows(sm.pbf[kSt], 32);
+#pragma unroll
+    for (int ks = 0; ks < kTile / 16; ++ks)
+        umma_f16(o + kColOR, dar + (ks * 2048) / 16, dpb + (16 * 32 * ks) / 16, kIdPVr, ks > 0 ? 1u : acc0);
+    umma_commit(&sm.imgempty[kBuf]);
+    umma_commit(&sm.pdone[kSt]);
+}
+// Tile T's stream is T % 2, its image T % 2 (fp4) or T % 3 (fp8): f(stream, image) as compile-time constants.
+template <bool kFp4, typename F>
+__device__ __forceinline__ void with_tile(int T, F&& f) {
+    if constexpr (kFp4) {
+        if (T & 1) f.template operator()<1, 1>();
+        else f.template operator()<0, 0>();
+    } else {
+        switch (T % 6) {
+            case 0: f.template operator()<0, 0>(); break;
+            case 1: f.template operator()<1, 1>(); break;
+            case 2: f.template operator()<0, 2>(); break;
+            case 3: f.template operator()<1, 0>(); break;
+            case 4: f.template operator()<0, 1>(); break;
+            default: f.template operator()<1, 2>(); break;
+        }
+    }
+}
+template <bool kFp4>
+struct IssueQk {
+    Smem<kFp4>& sm;
+    template <int kSt, int kBuf> __device__ __forceinline__ void operator()() { issue_qk<kFp4, kSt, kBuf>(sm); }
+};
+template <bool kFp4>
+struct IssuePv {
+    Smem<kFp4>& sm;
+    uint32_t acc0;
+    template <int kSt, int kBuf> __device__ __forceinline__ void operator()() { issue_pv<kFp4, kSt, kBuf>(sm, acc0); }
+};
+
 }  // namespace
 
 template <bool kFp4>
@@ -356,14 +420,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
         tmem_alloc(&sm.tmem_base, 512);
         tmem_relinquish();
     }
-    if (kFp4 && tid >= 512 && tid < 532) {   // table rows: 2^(6-j) times the E2M1 grid in E4M3
-        const int j = tid - 512;
-        const float s = j == kLutNan ? __uint_as_float(0x7FC00000u) : pow2f(6 - j);
+    if (kFp4 && tid >= 512 && tid < 512 + kLutRows) {   // table rows: 2^(6-j) times the E2M1 grid in E4M3
+        const int j = tid - 513;
+        const float s = j < 0 ? __uint_as_float(0x7FC00000u) : j == kLutRows - 2 ? 0.f : pow2f(6 - j);
         const float twice[8] = {0.f, 1.f, 2.f, 3.f, 4.f, 6.f, 8.f, 12.f};
         uint32_t w[2] = {0u, 0u};
 #pragma unroll
         for (int k = 0; k < 8; ++k) w[k >> 2] |= f32_to_e4m3(0.5f * twice[k] * s) << (8 * (k & 3));
-        sm.lut[j] = make_uint2(w[0], w[1]);
+        sm.lut[tid - 512] = make_uint2(w[0], w[1]);
     }
     if (!kFp4 && warp == kCopyWarp && lane == 0) tma_prefetch_map(&pages_map);
     tc_fence_before();
@@ -460,10 +524,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.qready);
                 named_barrier(kBarAll, 512);   // c2 of every head
-                float nm[8], l[8], g = 0.f;   // -m; g = 0: not set yet (fp4)
+                float nm[8], l[8], g = 0.f;   // nm = kUnset, g = 0: not set yet
 #pragma unroll
                 for (int h = 0; h < 8; ++h) {
-                    nm[h] = -kUnset;
+                    nm[h] = kUnset;
                     l[h] = 0.f;
                 }
                 const int T1 = T + wk.len;
@@ -484,19 +548,26 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
                         float top = t[0];
 #pragma unroll
                         for (int h = 1; h < 8; ++h) top = fmaxf(top, t[h]);
-                        over = top > (kFp4 ? kOver4 : kOver8) || (kFp4 && fe * g > kFeMost);
+                        over = top > kOver<kFp4> || (kFp4 && fe * g > kFeMost);
                         if (!__any_sync(0xffffffffu, over)) write_p<kFp4>(sm.p8[st], sm.pbf[st], t, fe >= 0.f ? fe * g : 0.f, hg, e);
                     }
                     fence_proxy_async_smem();
                     if (named_barrier_or(kBarStream + st, 256, over)) {
+                        // some weight is too large, or the first tile: the tile's maxima (of the logits themselves, nm
+                        // may be unset), every head that lies more than 2 above its mark set anew, O rescaled
                         const bool seen = fe >= 0.f;
                         if (sub < kTile / 32) {
-                            load_t<kFp4>(t, ts, c2, nm, fe, seen);
+                            float z[8];
+#pragma unroll
+                            for (int h = 0; h < 8; ++h) z[h] = 0.f;
+                            load_t<kFp4>(t, ts, c2, z, fe, seen);
+                            float mine = 0.f;
 #pragma unroll
                             for (int h = 0; h < 8; ++h) {
-                                const uint32_t km = __reduce_max_sync(0xffffffffu, score_key(t[h]));
-                                if (lane == h) sm.tmax[st][sub][8 * hg + h] = key_to_float(km);
+                                const float top = key_to_float(__reduce_max_sync(0xffffffffu, score_key(t[h])));
+                                mine = lane == h ? top : mine;
                             }
+                            if (lane < 8) sm.tmax[st][sub][8 * hg + lane] = mine;
                             if (kFp4 && hg == 0) {
                                 const uint32_t fm = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(fe, 0.f)));
                                 if (lane == 0) sm.femax[st][sub] = __uint_as_float(fm);
@@ -518,43 +589,19 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
                         }
 #pragma unroll
                         for (int h = 0; h < 8; ++h) {
-                            float tm = sm.tmax[st][0][8 * hg + h];   // relative to the old maximum
+                            float tm = sm.tmax[st][0][8 * hg + h];
 #pragma unroll
                             for (int q3 = 1; q3 < kTile / 32; ++q3) tm = fmaxf(tm, sm.tmax[st][q3][8 * hg + h]);
-                            const bool first = nm[h] == -kUnset, up = tm > (kFp4 ? kOver4 : kOver8);
-                            // a first maximum came out as x + 1e30, which lost x: it is formed below from S
-                            f[h] = up && !first ? exp2_ftz((kFp4 ? 0.f : kLift8) - tm) : 1.f;
-                            rescale |= up && !first;
+                            const bool first = nm[h] == kUnset;
+                            const bool set = first ? tm > -INFINITY : tm + nm[h] > kLift<kFp4> + 2.f;
+                            const float to_nm = set ? kLift<kFp4> - tm : nm[h];
+                            f[h] = set && !first ? exp2_ftz(to_nm - nm[h]) : 1.f;
+                            rescale |= set && !first;
                             l[h] *= f[h];
-                            if (up && !first) nm[h] -= tm - (kFp4 ? 0.f : kLift8);
-                        }
-                        bool unset = false;
-#pragma unroll
-                        for (int h = 0; h < 8; ++h) unset |= nm[h] == -kUnset;
-                        if (named_barrier_or(kBarStream + st, 256, unset)) {
-                            // some head has no maximum yet: the tile's own, from logits relative to zero
-                            float z[8];
-#pragma unroll
-                            for (int h = 0; h < 8; ++h) z[h] = 0.f;
-                            if (sub < kTile / 32) {
-                                load_t<kFp4>(t, ts, c2, z, fe, seen);
-#pragma unroll
-                                for (int h = 0; h < 8; ++h) {
-                                    const uint32_t km = __reduce_max_sync(0xffffffffu, score_key(t[h]));
-                                    if (lane == h) sm.tmax[st][sub][8 * hg + h] = key_to_float(km);
-                                }
-                            }
-                            named_barrier(kBarStream + st, 256);
-#pragma unroll
-                            for (int h = 0; h < 8; ++h) {
-                                float tm = sm.tmax[st][0][8 * hg + h];
-#pragma unroll
-                                for (int q3 = 1; q3 < kTile / 32; ++q3) tm = fmaxf(tm, sm.tmax[st][q3][8 * hg + h]);
-                                if (nm[h] == -kUnset && tm > -INFINITY) nm[h] = (kFp4 ? 0.f : kLift8) - tm;
-                            }
+                            nm[h] = to_nm;
                         }
                         if (rescale) {   // the same answer in every thread of the head group
-#pragma unroll 1
+#pragma unroll 2
                             for (int c = 0; c < 13; ++c) {   // 4 blocks of 3 terms, then RoPE
                                 uint32_t o[8];
                                 const float fc = c < 12 ? fg : 1.f;
@@ -567,7 +614,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
                             tmem_st_wait();
                         }
                         if (sub < kTile / 32) {
-                            load_t<kFp4>(t, ts, c2, nm, fe, seen);
+#pragma unroll
+                            for (int h = 0; h < 8; ++h) t[h] += nm[h];
                             write_p<kFp4>(sm.p8[st], sm.pbf[st], t, seen ? fe * g : 0.f, hg, e);
                         }
                         fence_proxy_async_smem();
@@ -706,16 +754,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
                     const bool vis = ok && seen(e);
                     if constexpr (kFp4) {
                         const uint8_t* ch = sm.stage[buf] + ck * kChunk4Bytes;
-                        const uint32_t base = ch[kChunk4Exp + kGroups * kChunk + tk];
-                        if (part == 0) sm.fe[buf][e] = vis ? ldexpf(1.f, static_cast<int>(base) - 133) : -1.f;
+                        const int ex0 = ch[kChunk4Exp + kGroups * kChunk + tk];
+                        if (part == 0) sm.fe[buf][e] = vis ? ldexpf(1.f, ex0 - 133) : -1.f;
+                        const int base = vis ? ex0 : 4096;
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const int g = part + 4 * i;
                             if (g >= kGroups) break;   // whole warps
-                            uint4 w = *reinterpret_cast<const uint4*>(ch + g * 256 + tk * 16);
-                            const uint32_t ex = ch[kChunk4Exp + g * kChunk + tk];
-                            if (!vis) w = make_uint4(0, 0, 0, 0);
-                            const uint2 tab = vis ? sm.lut[ex == 255 ? kLutNan : min(base - ex, 18u)] : make_uint2(0, 0);
+                            const uint4 w = *reinterpret_cast<const uint4*>(ch + g * 256 + tk * 16);
+                            const int ex = ch[kChunk4Exp + g * kChunk + tk];   // 255 (NaN) is above every base
+                            const uint2 tab = sm.lut[1 + max(-1, min(base - ex, kLutRows - 2))];
                             uint4 a, b;
                             decode8(w.x, tab, a.x, a.y);
                             decode8(w.y, tab, a.z, a.w);
@@ -794,32 +842,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
             }
         } else if (lane == 0) {
             // ===== MMA issue ==================================================================================
-            const uint64_t dq = desc_sw128(sm.qk[0], 0), dqr = desc_sw128(sm.qr, 0);
+            if (tmem != 0) *fail = 1;   // the MMAs' column constants
             Walk wp = wk;                              // the walks of QK and of PV
             int nq = 0, np = 0, qt = 0, pt = 0, seg = 0;   // running tiles, tiles within the segments
             uint32_t idle = 0;
             while (np < n_tiles) {
                 if (*fail) break;
                 if (np < nq && mbar_test(&sm.pfull[np & 1], (np >> 1) & 1)) {
-                    const int st = np & 1, buf = np % kBufs;
                     tc_fence_after();
-                    const uint32_t acc0 = pt >= 2 ? 1u : 0u;   // the stream's first tile of the segment overwrites O
-                    const uint64_t da = desc_sw128(sm.img[buf], 0), dp = desc_rows(sm.p8[st], 64);
-                    const uint32_t o = tmem + kColO + kStepO * st;
-#pragma unroll
-                    for (int mb = 0; mb < 4; ++mb)
-#pragma unroll
-                        for (int kb = 0; kb < kKBlocks; ++kb)
-                            umma_f8f6f4(o + 48u * mb, da + (mb * kBlkBytes + kb * 4096) / 16, dp + (32 * 64 * kb) / 16, kIdPV,
-                                        kb > 0 ? 1u : acc0);
-                    const uint64_t dar = desc_sw128(sm.img[buf] + kRopeBlk * kBlkBytes, kBlkBytes);
-                    const uint64_t dpb = desc_rows(sm.pbf[st], 32);
-#pragma unroll
-                    for (int ks = 0; ks < kTile / 16; ++ks)
-                        umma_f16(o + kColOR, dar + (ks * 2048) / 16, dpb + (16 * 32 * ks) / 16, kIdPVr,
-                                 ks > 0 ? 1u : acc0);
-                    umma_commit(&sm.imgempty[buf]);
-                    umma_commit(&sm.pdone[st]);
+                    with_tile<kFp4>(np, IssuePv<kFp4>{sm, pt >= 2 ? 1u : 0u});   // a stream's first tile of a segment overwrites O
                     ++np;
                     if (++pt == wp.len) {
                         pt = 0;
@@ -830,21 +861,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
                 }
                 if (nq < n_tiles && nq < np + 2 && mbar_test(&sm.imgfull[nq % kBufs], (nq / kBufs) & 1) &&
                     (qt > 0 || mbar_test(&sm.qready, seg & 1))) {
-                    const int st = nq & 1;
                     tc_fence_after();
-                    const uint32_t d = tmem + kColS + kStepS * st;
-                    const uint64_t da = desc_sw128(sm.img[nq % kBufs], 0);
-#pragma unroll
-                    for (int kb = 0; kb < 4; ++kb)
-#pragma unroll
-                        for (int ks = 0; ks < (kb < 3 ? 4 : 2); ++ks)
-                            umma_f8f6f4(d, da + (kb * kBlkBytes + 32 * ks) / 16, dq + (kb * 4096 + 32 * ks) / 16, kIdQK,
-                                        (kb | ks) != 0 ? 1u : 0u);
-#pragma unroll
-                    for (int ks = 0; ks < 4; ++ks)   // fp4: apart, since f_e multiplies only the 4-bit dims
-                        umma_f16(d + (kFp4 ? 32u : 0u), da + (kRopeBlk * kBlkBytes + 32 * ks) / 16, dqr + (32 * ks) / 16, kIdQKr,
-                                 kFp4 && ks == 0 ? 0u : 1u);
-                    umma_commit(&sm.sfull[st]);
+                    with_tile<kFp4>(nq, IssueQk<kFp4>{sm});
                     ++nq;
                     if (++qt == wk.len) {
                         qt = 0;
