@@ -1,38 +1,47 @@
 // Attention over the paged entry cache: a sliding window with first tokens that stay visible, or every
-// token (layouts: csld_paged_cache in csld.h), on the 5th-generation tensor cores.
+// token (layouts: csld_paged_cache in csld.h).
 //
 // Source: "DeepSeek-V4: a million-token context that agents can actually use" -- CSA and HCA paragraphs
 // (a sliding-window branch over the most recent uncompressed tokens), storage paragraph (entries in low
 // precision except the RoPE dims in bf16; FP4 where it suffices), layer-pattern paragraph (the
 // window-only multi-token-prediction block).
 //
-// out_h = sum_t p_t k_t / l,  p_t = 2^(scale log2(e) q_h.k_t - m),  l = sum_t p_t over the visible tokens t,
+// out_h = sum_t p_t k_t / l,  p_t = 2^(scale log2(e) q_h.k_t + nm),  l = sum_t p_t over the visible tokens t,
 // keys = values = the 512-d entry, 16 heads of one query at a time.
 //
 // Work.  A row is one (sequence, query, group of 16 heads).  Its token list is made of 16-token chunks, each
-// inside one page: the chunks of the first tokens, then those of the window (or all), six chunks to a tile.
+// inside one page: the chunks of the first tokens, then those of the window (or all), four chunks to a tile.
 // The tiles of all rows, row after row, are dealt out evenly to one CTA per SM, so sequences of any mix of
 // lengths load the SMs alike; a CTA walks its share as segments of rows.  A row that lies whole in one share is
 // written out directly; of a row cut by shares each CTA leaves its unnormalised O and (m, l), and
 // paged_merge_kernel joins them.
 //
-// A CTA's 24 warps:
-//   copy     (warp 22)     pages -> shared memory, bulk copies (fp4: a chunk is 5888 contiguous bytes, staged
-//                          as it lies) or tensor-map boxes with the 128-byte swizzle (fp8, into the tile image)
-//   convert  (warps 16-21) fp4: codes -> E4M3 bytes in the swizzled tile image.  A 16-byte group of 32 codes is
-//                          turned by byte permutes through an 8-byte table of 2^(6-j) times the E2M1 grid, j =
-//                          the entry's largest exponent minus the group's, so an entry's image is its values
-//                          over one power of two f_e (exact for j <= 14: 0.5 * 2^-8 is E4M3's smallest step).
-//                          Both formats: rows of masked or missing tokens are zeroed, whatever was in them.
-//   MMA      (warp 23)     S[entry][head] = K Q^T and O^T[dim][head] += V^T P from the one image: E4M3 keys against
-//                          the query as two E4M3 terms (exact for bf16), values against the weights as two E4M3
-//                          terms with a block scale per 32 entries, RoPE dims in bf16
-//   softmax  (warps 0-15)  two streams of 8 warps take the tiles in turn, each with its own running maximum, sum and
-//                          O (all in tensor memory), so that one stream's softmax runs under the other's MMAs;
-//                          they are joined when a segment ends.  A thread owns one entry and 8 heads.  f_e
-//                          multiplies S and P per entry, outside the MMAs.  The maximum is raised lazily: only
-//                          where a tile exceeds it by 2^8 is O rescaled.
-// Every wait is bounded; a wait that gives up sets CSLD_DEVERR_TIMEOUT and all roles run out without waiting.
+// Which tensor instructions.  With 16 heads one side of every product is 16 rows.  A tcgen05.mma reads its
+// 128-row operand, here the entries, from shared memory at 128 B a cycle: 45 cycles for 128 x 32 x 32 (measured;
+// 16 at full rate), and a version of this kernel built on it moved 326 KB through shared memory for 96 fp4
+// entries and took 3000 cycles (1M fp4 tokens 222 us).  The warp-level E4M3 mma.sync runs at 3800 MAC a cycle
+// and SM (measured) with its operands in registers: the query stays there for a whole row, 4-bit keys go from a
+// code word to a B fragment without touching shared memory, and only the values take that way.
+//
+// A CTA's roles (16 warps; registers moved from the copy warps to the score warps):
+//   copy   (warp 12)    pages -> a ring of tiles in shared memory: fp4 chunks as they lie (5888 contiguous bytes, bulk
+//                       copies), fp8 entries as five 128-byte column blocks with the 128-byte swizzle (tensor map)
+//   score  (warps 0-3)  warp w takes the tile's chunk w.  S = Q K^T by m16n8k32 E4M3 MMAs, the bf16 query as two E4M3
+//                       terms (exact: 4 + 4 significant bits and a sign), the RoPE dims by bf16 MMAs.  fp4: lane
+//                       (n, c) = (lane / 4, lane % 4) decodes word c of entry n's group: its 8 codes are that
+//                       lane's whole share of the group's 32-dim MMA step, in whatever order, since the query's
+//                       dims are laid out the same.  E2M1 -> E4M3 is a byte permute through 8 table bytes, 2^(6-j)
+//                       times the grid, j = the entry's largest exponent minus the group's: all normal numbers, so
+//                       j only subtracts 8 j from each (j > 11 or a NaN group: from a table in shared memory); an
+//                       entry's decoded bytes are its values over one power of two f_e, applied to S and to P.
+//                       The decoded bytes also go to the value image.  Then the softmax: p relative to a mark nm that
+//                       is only raised when some p exceeds 2^10..15, one meeting of the four warps a tile, and P as
+//                       A fragments in shared memory: p f_e as three E5M2 terms, p as bf16 for the RoPE dims.
+//   value  (warps 4-11) warp w owns 64 of the 512 dims and keeps its O in registers: O += P V by m16n8k32 E5M2 x E4M3
+//                       MMAs, V fragments by transposing 8-bit matrix loads of the image (fp8: of the copied tile
+//                       itself); warp 11 the RoPE dims, bf16
+// Rows of masked or missing tokens are zeroed before they are used, whatever was in them.  Every wait is
+// bounded; a wait that gives up sets CSLD_DEVERR_TIMEOUT and all roles run out without waiting.
 #include <stdint.h>
 
 #include "kernels.cuh"
@@ -43,51 +52,38 @@ namespace csld {
 
 namespace {
 
-constexpr int kThreads = 960;
-constexpr int kConvWarp = 16, kConvWarps = 12, kCopyWarp = 28, kMmaWarp = 29;
-constexpr int kTile = 96;                        // entries per tile
-constexpr int kTileChunks = kTile / kChunk;      // 6
+constexpr int kThreads = 512;
+constexpr int kScoreWarps = 4, kValueWarp = 4, kValueWarps = 8, kCopyWarp = 12;
+// registers a thread: the launch gives 512 x 128 = 65,536; 128 x 216 + 256 x 120 + 128 x 40 = 63,488
+constexpr int kRegsScore = 216, kRegsValue = 120, kRegsCopy = 40;
+constexpr int kTile = 64, kTileChunks = kTile / kChunk;   // entries per tile; a chunk per score warp
+static_assert(kTileChunks == kScoreWarps, "score warp w takes chunk w");
 constexpr int kBlkBytes = kTile * 128;           // one 128-byte column block of a tile
-constexpr int kRopeBlk = 4;
-constexpr int kImgBytes = 5 * kBlkBytes;         // 60 KB
-constexpr int kStageBytes = kTileChunks * kChunk4Bytes;
-constexpr int kKBlocks = kTile / 32;
-// Weights: p = 2^(x + nm); a head's nm is set so that the largest p of a tile is 2^kLift and kept until one exceeds
-// 2^kOver.  The PV operand holds p w in E5M2, w = 1 (fp8) or f_e g (fp4; g a power of two set so that the tile's
-// largest f_e g is kFeSet, kept until one exceeds kFeMost).  E5M2 bounds the product: 57344 > 2^kOver w.
+constexpr int kImgBytes = 5 * kBlkBytes;         // dims 0..127, 128..255, 256..383, 384..447, RoPE
+constexpr int kSteps = kGroups;                  // 32-dim steps of the 448 dims
+// Marks: a head's nm is set so that the largest p of a tile is 2^kLift and kept until one exceeds 2^kOver.  The
+// operand holds p w in f16, w = 1 (fp8) or f_e g (fp4; g a power of two set so that the tile's largest f_e g is
+// kFeSet, kept until one exceeds kFeMost).  f16 bounds the product: 2^kOver w <= 2^15.
 template <bool kFp4> constexpr float kLift = kFp4 ? 0.f : 5.f;
 template <bool kFp4> constexpr float kOver = kFp4 ? 10.f : 15.f;
 constexpr float kFeSet = 8.f, kFeMost = 32.f, kUnset = 1e30f;
-// tensor-memory columns of stream s: S at kColS + 48 s (16 hi, 16 lo, 16 RoPE), O at kColO + 208 s (four dim blocks
-// of 48: the three terms of P; RoPE 16)
-constexpr uint32_t kColS = 0, kStepS = 48, kColO = 96, kStepO = 208, kColOR = 192;
-constexpr uint32_t kIdQK = idesc_e4m3_m128(32, false, false);
-constexpr uint32_t kIdQKr = idesc_bf16_m128(16, false, false);
-constexpr uint32_t kIdPV = idesc_e4m3_m128(48, true, true) | (1u << 10);   // B in E5M2
-constexpr uint32_t kIdPVr = idesc_bf16_m128(16, true, true);
-constexpr int kBarStream = 1, kBarAll = 3;       // named barriers: the streams' (1, 2), both streams' (3)
-constexpr int kLutRows = 21;                     // NaN group; j = 0..18; all zero (j >= 19, masked entries)
+constexpr int kBarScore = 1;                     // named barrier of the score warps
 
 template <bool kFp4>
 struct Smem {
-    static constexpr int kBufs = kFp4 ? 2 : 3;   // tile images
-    uint8_t img[kBufs][kImgBytes];               // [block][entry][128 B], 128-byte swizzle
-    uint8_t qk[4][32 * 128];                     // QK B operand per dim block: rows 0..15 Qhi, 16..31 Qlo (the MMAs also
-                                                 // read past the last image into here: rows whose results go unused)
-    uint8_t qr[16 * 128];                        // RoPE query
-    uint8_t p8[2][kTile * 64];                   // per stream: PV B operand [entry][16 heads x 3 terms], 64-byte swizzle
-    uint8_t pbf[2][kTile * 32];                  // per stream: bf16 P [entry][16 heads], 32-byte swizzle
-    uint8_t stage[kFp4 ? 2 : 1][kFp4 ? kStageBytes : 16];
-    uint2 lut[kLutRows];
-    alignas(16) float fe[kBufs][kTile];          // entry factors; -1: masked (before the walk: the scan's sums)
-    alignas(16) float c2[kHeads];
-    alignas(16) float tmax[2][4][kHeads];        // per stream: tile maxima (then partial sums) per lane quarter
-    float femax[2][4], ginv[2];                  // per stream: largest f_e per lane quarter; 1 / g
-    float2 ml[2][kHeads];
-    int32_t chunk_tok[kBufs][kTileChunks];       // first token of a tile's chunks; -1: none
-    uint64_t stfull[kBufs], stempty[2], imgfull[kBufs], imgempty[kBufs], sfull[2], pfull[2], pdone[2], qready, drain;
-    int64_t prefix;
-    uint32_t tmem_base;
+    static constexpr int kStages = 5;
+    static constexpr int kStageBytes = kFp4 ? kTileChunks * kChunk4Bytes : kImgBytes;
+    uint8_t img[kFp4 ? 2 : 1][kFp4 ? kImgBytes : 1024];   // fp4: value images [block][entry][128 B], 128-byte swizzle
+    uint8_t stage[kStages][kStageBytes];         // fp8: the same layout, as copied
+    uint4 p16[2][kTileChunks][32];               // P in f16: [chunk][lane] A fragments
+    uint4 pbf[2][kTileChunks][32];               // bf16 P: [chunk][lane]
+    float fn[2][kHeads], fr[2][kHeads];          // factors of O before a tile's MMAs (448 dims; RoPE dims)
+    float tmax[kScoreWarps][kHeads], femax[kScoreWarps];
+    float lsum[2][kScoreWarps][kHeads], mseg[2][kHeads], ginv[2];   // a segment's sums, marks and 1 / g
+    int32_t chunk_tok[kStages][kTileChunks];     // first token of a tile's chunks; -1: none
+    int32_t resc[2];                             // 0: O stays, 1: O *= f, 2: O = 0 (first tile of a segment)
+    uint64_t full[kStages], empty[kStages], pfull[2], pempty[2], segfull[2], segempty[2];
+    int64_t red[kThreads / 32], prefix;
     int32_t fail, b0, n_issued;
 };
 static_assert(sizeof(Smem<true>) <= 232448 && sizeof(Smem<false>) <= 232448, "227 KB of shared memory");
@@ -106,14 +102,6 @@ struct Params {
     bool out_bf16;
 };
 
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-        " selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
-    return ok != 0;
-}
 // Bounded wait: false once any wait of the CTA has given up (this one after about a second).
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int32_t* fail) {
     for (uint32_t i = 0; i < (1u << 22); ++i) {
@@ -127,14 +115,30 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
     return false;
 }
 __device__ __forceinline__ float pow2f(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
-__device__ __forceinline__ float key_to_float(uint32_t k) {
-    return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
-}
 __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
     asm volatile(
         "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
         :: "r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar)) : "memory");
 }
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Two 16 x 16 byte matrices, transposed: lane i gives the address of row i (16 B).  r0, r2: bytes of rows 4 (lane % 4)
+// .. + 3 of the first and second matrix at column lane / 4; r1, r3: at column 8 + lane / 4.
+__device__ __forceinline__ void ldmatrix_b8_trans_x2(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+__device__ __forceinline__ void ldmatrix_b16_trans_x4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+template <int kRegs>
+__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs)); }
+template <int kRegs>
+__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs)); }
 
 // ---- the token list of a sequence -----------------------------------------------------------
 // n tokens; chunks [0, cs) hold the first tokens, then come the chunks from wl on, nc in all; tiles per row.
@@ -192,199 +196,509 @@ __device__ __forceinline__ bool sees(const Params& P, int t, int p) {
     return t <= p && (P.W == 0 || t < P.sinks || t > p - P.W);
 }
 
-// ---- convert: eight E2M1 codes (one word) -> eight E4M3 bytes ---------------------------------
+// ---- numbers --------------------------------------------------------------------------------
+// Eight E2M1 codes (one word) -> eight bytes of the table tab with the codes' signs.
 __device__ __forceinline__ void decode8(uint32_t w, uint2 tab, uint32_t& lo, uint32_t& hi) {
     const uint32_t sel = w & 0x77777777u;
     lo = __byte_perm(tab.x, tab.y, sel) | (w & 0x80808080u);
     hi = __byte_perm(tab.x, tab.y, sel >> 16) | ((w << 4) & 0x80808080u);
 }
+// 2^13 times the E2M1 grid (0, 4096, 8192, 12288, 16384, 24576, 32768, 49152) in E5M2, and what a factor of 1/2 takes off.
+constexpr uint32_t kTabX = 0x72706C00u, kTabY = 0x7A787674u, kTabDx = 0x04040400u, kTabDy = 0x04040404u;
+constexpr int kMaxJ = 26;                        // the table's smallest entry stays a normal number
 
-// ---- softmax ----------------------------------------------------------------------------------
-// t = x - m for this thread's 8 heads (log2 units; nm = -m), -inf where the entry is masked.
-template <bool kFp4>
-__device__ __forceinline__ void load_t(float (&t)[8], uint32_t ts, const float* c2, const float (&nm)[8], float fe, bool seen) {
-    uint32_t hi[8], lo[8], r[8];
-    tmem_ld_32x32b_x8(ts, hi);
-    tmem_ld_32x32b_x8(ts + 16u, lo);
-    if constexpr (kFp4) tmem_ld_32x32b_x8(ts + 32u, r);
-    tmem_ld_wait();
-    const float4 ca = *reinterpret_cast<const float4*>(c2), cb = *reinterpret_cast<const float4*>(c2 + 4);
-    const float c[8] = {ca.x, ca.y, ca.z, ca.w, cb.x, cb.y, cb.z, cb.w};
-#pragma unroll
-    for (int h = 0; h < 8; ++h) {
-        float v = __uint_as_float(hi[h]) + __uint_as_float(lo[h]);
-        if constexpr (kFp4) v = fmaf(v, fe, __uint_as_float(r[h]));
-        t[h] = seen ? fmaf(v, c[h], nm[h]) : -INFINITY;
-    }
+// Two bytes of v, E5M2 or E4M3, as two f16 (exact).  E5M2 is f16's upper byte.
+template <bool kE5M2, int kHalf>
+__device__ __forceinline__ uint32_t bytes_to_f16x2(uint32_t v) {
+    if constexpr (kE5M2) return __byte_perm(v, 0u, kHalf ? 0x3424 : 0x1404);
+    else return e4m3x2_to_f16x2(kHalf ? v >> 16 : v & 0xFFFFu);
 }
 __device__ __forceinline__ uint32_t f32x2_to_f16x2(float a, float b) {
     const __half2 v = __floats2half2_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&v);
 }
-// Two f16 -> two E5M2 bytes (round to nearest even).  E5M2 is f16's upper byte, so the way back is a byte permute.
-__device__ __forceinline__ uint32_t f16x2_to_e5m2x2(uint32_t v) {
-    uint16_t r;
-    asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(v));
-    return r;
-}
-__device__ __forceinline__ uint32_t f16x2_sub(uint32_t a, uint32_t b) {
-    const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
-    return *reinterpret_cast<const uint32_t*>(&v);
-}
-// t <- p = 2^t, and p into the PV operands of this entry: p w (w = f_e g; fp8: p itself) as f16 and from there as
-// three E5M2 terms, each the rounding of what the ones before left (2^-3 of it: 2^-9 in all, and nothing finer
-// than E5M2's 2^-16, 2^-23 of the largest weight), 8 heads a store; p in bf16 for the RoPE dims.
-template <bool kFp4>
-__device__ __forceinline__ void write_p(uint8_t* p8, uint8_t* pb, float (&t)[8], float w, int hg, int e) {
-    uint32_t term[3][2], bf[4];
-#pragma unroll
-    for (int h = 0; h < 8; h += 4) {
-        uint32_t v[2], q[3][2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int k = h + 2 * u;
-            t[k] = exp2_ftz(t[k]);
-            t[k + 1] = exp2_ftz(t[k + 1]);
-            bf[k >> 1] = f32x2_to_bf16x2_bits(t[k], t[k + 1]);
-            v[u] = kFp4 ? f32x2_to_f16x2(t[k] * w, t[k + 1] * w) : f32x2_to_f16x2(t[k], t[k + 1]);
-#pragma unroll
-            for (int n = 0; n < 3; ++n) {
-                q[n][u] = f16x2_to_e5m2x2(v[u]);
-                if (n < 2) v[u] = f16x2_sub(v[u], __byte_perm(q[n][u], 0u, 0x1404));   // exact
-            }
-        }
-#pragma unroll
-        for (int n = 0; n < 3; ++n) term[n][h >> 2] = __byte_perm(q[n][0], q[n][1], 0x5410);
-    }
-    const int sw = (e >> 1) & 3;
-#pragma unroll
-    for (int n = 0; n < 3; ++n)
-        *reinterpret_cast<uint2*>(p8 + 64 * e + 16 * (n ^ sw) + 8 * hg) = make_uint2(term[n][0], term[n][1]);
-    *reinterpret_cast<uint4*>(pb + 32 * e + 16 * (hg ^ ((e >> 2) & 1))) = make_uint4(bf[0], bf[1], bf[2], bf[3]);
-}
-// MN-major operand of rows of 64 or 32 bytes under the swizzle of that width: 8-row groups one after the other.
-__device__ __forceinline__ uint64_t desc_rows(const void* p, uint32_t row_bytes) {
-    uint64_t d = static_cast<uint64_t>((smem_u32(p) >> 4) & 0x3FFFu);
-    d |= static_cast<uint64_t>((8 * row_bytes) >> 4) << 32;
-    d |= static_cast<uint64_t>(1u) << 46;
-    d |= static_cast<uint64_t>(row_bytes == 64 ? 4u : 6u) << 61;
-    return d;
-}
 
-// The query of one head as MMA operands, one warp per head, 16 dims per lane: scaled by a power of two so that
-// its largest value lies in 2^7..2^8, then (dims 0..447) two E4M3 terms -- bf16's 8 significant bits split
-// exactly, down to 2^-10 of the largest -- or (RoPE) bf16.
-template <bool kFp4>
-__device__ __forceinline__ void prepare_query(Smem<kFp4>& sm, const uint4 (&v)[2], int h, int lane, float scale) {
-    const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
-    uint32_t top = 0;
+// ---- the query ---------------------------------------------------------------------------------
+// A fragments of 16 heads' queries: lane (g, c) holds heads g and g + 8, of every 32-dim step the dims 8c..8c+7
+// (f16: two 16-dim MMA steps, the dims in the order that the lane's eight key bytes come in), of every 16-dim
+// RoPE step the dims 4c..4c+3 (bf16), scaled per head by a power of two so that its largest value lies in
+// 2^7..2^8: exact in f16 down to 2^-21 of it.
+struct Query {
+    uint32_t f[kSteps][2][4], rope[4][4];
+    float c2[2];         // logit factor (log2 units) of the two heads
+    __device__ __forceinline__ void load(const Params& P, int b, int rq, int g, int c) {
+        const int j = rq / P.groups, h0 = 16 * (rq % P.groups) + g;
+        const uint16_t* q0 = P.q + (((int64_t)b * P.Q + j) * P.heads + h0) * kDim;
+        uint32_t top[2] = {0, 0};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
-    top = __reduce_max_sync(0xffffffffu, top);
-    const int sh = top ? max(-100, min(100, 7 - (static_cast<int>(top >> 7) - 127))) : 0;
-    const float sq = pow2f(sh);
-    if (lane == 0) sm.c2[h] = scale * 1.4426950408889634f / sq;
-    if (lane < kNope / 16) {
-        uint32_t hw[4], lw[4];
+        for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const uint4 v = h0 + 8 * r < P.heads ? __ldg(reinterpret_cast<const uint4*>(q0 + 8 * r * kDim + 32 * s + 8 * c))
+                                                     : make_uint4(0, 0, 0, 0);
+                f[s][0][r] = v.x;
+                f[s][0][2 + r] = v.y;
+                f[s][1][r] = v.z;
+                f[s][1][2 + r] = v.w;
+            }
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const uint2 v = h0 + 8 * r < P.heads
+                                    ? __ldg(reinterpret_cast<const uint2*>(q0 + 8 * r * kDim + kNope + 16 * s + 4 * c)) : make_uint2(0, 0);
+                rope[s][r] = v.x;
+                rope[s][2 + r] = v.y;
+            }
+        auto peak = [&](int i, uint32_t x) { top[i & 1] = max(top[i & 1], max(x & 0x7FFFu, (x >> 16) & 0x7FFFu)); };
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            uint32_t hi2[2], lo2[2];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const uint32_t x = w[2 * i + u];
-                const float x0 = bf16_bits_to_f32(x) * sq, x1 = bf16_bits_to_f32(x >> 16) * sq;
-                hi2[u] = __nv_cvt_float2_to_fp8x2(make_float2(x0, x1), __NV_SATFINITE, __NV_E4M3);
-                const uint32_t back = e4m3x2_to_f16x2(hi2[u]);
-                lo2[u] = __nv_cvt_float2_to_fp8x2(
-                    make_float2(x0 - __half2float(__ushort_as_half(static_cast<unsigned short>(back & 0xFFFFu))),
-                                x1 - __half2float(__ushort_as_half(static_cast<unsigned short>(back >> 16)))),
-                    __NV_SATFINITE, __NV_E4M3);
+            for (int s = 0; s < kSteps; ++s) {
+                peak(i, f[s][0][i]);
+                peak(i, f[s][1][i]);
             }
-            hw[i] = (hi2[0] & 0xFFFFu) | (hi2[1] << 16);
-            lw[i] = (lo2[0] & 0xFFFFu) | (lo2[1] << 16);
+#pragma unroll
+            for (int s = 0; s < 4; ++s) peak(i, rope[s][i]);
         }
-        uint8_t* blk = sm.qk[lane >> 3];
-        const int c = 16 * (lane & 7);
-        *reinterpret_cast<uint4*>(blk + sw128(h, c)) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
-        *reinterpret_cast<uint4*>(blk + sw128(16 + h, c)) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
-    } else {
-        uint32_t o[8];
+        float sq[2];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = f32x2_to_bf16x2_bits(bf16_bits_to_f32(w[i]) * sq, bf16_bits_to_f32(w[i] >> 16) * sq);
-        const int c = 32 * (lane - kNope / 16);
-        *reinterpret_cast<uint4*>(sm.qr + sw128(h, c)) = make_uint4(o[0], o[1], o[2], o[3]);
-        *reinterpret_cast<uint4*>(sm.qr + sw128(h, c + 16)) = make_uint4(o[4], o[5], o[6], o[7]);
-    }
-    fence_proxy_async_smem();
-}
-
-__device__ __forceinline__ void store_out(const Params& P, int64_t at, float v) {
-    if (P.out_bf16) reinterpret_cast<uint16_t*>(P.out)[at] = static_cast<uint16_t>(f32_to_bf16_bits(v));
-    else reinterpret_cast<float*>(P.out)[at] = v;
-}
-
-// The MMAs of one tile.  Stream and image are compile-time constants and tensor memory starts at column 0 (all of it
-// is allocated), so descriptors are constants over one base: forming them at run time cost the issuing thread about
-// 95 cycles an MMA, twice what the tensor pipe takes for these narrow ones (45).
-template <bool kFp4, int kSt, int kBuf>
-__device__ __forceinline__ void issue_qk(Smem<kFp4>& sm) {
-    const uint64_t da = desc_sw128(sm.img[kBuf], 0), dq = desc_sw128(sm.qk[0], 0), dqr = desc_sw128(sm.qr, 0);
-    constexpr uint32_t d = kColS + kStepS * kSt;
+        for (int r = 0; r < 2; ++r) {
+            top[r] = max(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
+            top[r] = max(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
+            const int sh = top[r] ? max(-100, min(100, 134 - static_cast<int>(top[r] >> 7))) : 0;
+            sq[r] = pow2f(sh);
+            c2[r] = P.scale * 1.4426950408889634f / sq[r];
+        }
 #pragma unroll
-    for (int kb = 0; kb < 4; ++kb)
+        for (int i = 0; i < 4; ++i) {
 #pragma unroll
-        for (int ks = 0; ks < (kb < 3 ? 4 : 2); ++ks)
-            umma_f8f6f4(d, da + (kb * kBlkBytes + 32 * ks) / 16, dq + (kb * 4096 + 32 * ks) / 16, kIdQK, (kb | ks) != 0 ? 1u : 0u);
+            for (int s = 0; s < kSteps; ++s)
 #pragma unroll
-    for (int ks = 0; ks < 4; ++ks)   // fp4: apart, since f_e multiplies only the 4-bit dims
-        umma_f16(d + (kFp4 ? 32u : 0u), da + (kRopeBlk * kBlkBytes + 32 * ks) / 16, dqr + (32 * ks) / 16, kIdQKr,
-                 kFp4 && ks == 0 ? 0u : 1u);
-    umma_commit(&sm.sfull[kSt]);
-}
-template <bool kFp4, int kSt, int kBuf>
-__device__ __forceinline__ void issue_pv(Smem<kFp4>& sm, uint32_t acc0) {   // acc0 = 0: O is overwritten
-    const uint64_t da = desc_sw128(sm.img[kBuf], 0), dp = desc_rows(sm.p8[kSt], 64);
-    constexpr uint32_t o = kColO + kStepO * kSt;
+                for (int u = 0; u < 2; ++u)
+                    f[s][u][i] = f32x2_to_f16x2(bf16_bits_to_f32(f[s][u][i]) * sq[i & 1], bf16_bits_to_f32(f[s][u][i] >> 16) * sq[i & 1]);
 #pragma unroll
-    for (int mb = 0; mb < 4; ++mb)
-#pragma unroll
-        for (int kb = 0; kb < kKBlocks; ++kb)
-            umma_f8f6f4(o + 48u * mb, da + (mb * kBlkBytes + kb * 4096) / 16, dp + (32 * 64 * kb) / 16, kIdPV, kb > 0 ? 1u : acc0);
-    const uint64_t dar = desc_sw128(sm.img[kBuf] + kRopeBlk * kBlkBytes, kBlkBytes), dpb = desc_rows(sm.pbf[kSt], 32);
-#pragma unroll
-    for (int ks = 0; ks < kTile / 16; ++ks)
-        umma_f16(o + kColOR, dar + (ks * 2048) / 16, dpb + (16 * 32 * ks) / 16, kIdPVr, ks > 0 ? 1u : acc0);
-    umma_commit(&sm.imgempty[kBuf]);
-    umma_commit(&sm.pdone[kSt]);
-}
-// Tile T's stream is T % 2, its image T % 2 (fp4) or T % 3 (fp8): f(stream, image) as compile-time constants.
-template <bool kFp4, typename F>
-__device__ __forceinline__ void with_tile(int T, F&& f) {
-    if constexpr (kFp4) {
-        if (T & 1) f.template operator()<1, 1>();
-        else f.template operator()<0, 0>();
-    } else {
-        switch (T % 6) {
-            case 0: f.template operator()<0, 0>(); break;
-            case 1: f.template operator()<1, 1>(); break;
-            case 2: f.template operator()<0, 2>(); break;
-            case 3: f.template operator()<1, 0>(); break;
-            case 4: f.template operator()<0, 1>(); break;
-            default: f.template operator()<1, 2>(); break;
+            for (int s = 0; s < 4; ++s)
+                rope[s][i] = f32x2_to_bf16x2_bits(bf16_bits_to_f32(rope[s][i]) * sq[i & 1], bf16_bits_to_f32(rope[s][i] >> 16) * sq[i & 1]);
         }
     }
+};
+
+__device__ __forceinline__ void store_out2(const Params& P, int64_t at, float a, float b) {
+    if (P.out_bf16) *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(P.out) + at) = f32x2_to_bf16x2_bits(a, b);
+    else *reinterpret_cast<float2*>(reinterpret_cast<float*>(P.out) + at) = make_float2(a, b);
 }
+
+// ---- score warps ---------------------------------------------------------------------------------
 template <bool kFp4>
-struct IssueQk {
-    Smem<kFp4>& sm;
-    template <int kSt, int kBuf> __device__ __forceinline__ void operator()() { issue_qk<kFp4, kSt, kBuf>(sm); }
-};
+__device__ __forceinline__ void score_role(Smem<kFp4>& sm, const Params& P, Walk wk, int w, int lane, int64_t u1, int64_t n_cta,
+                                           int64_t total) {
+    constexpr int kStages = Smem<kFp4>::kStages;
+    volatile int32_t* fail = &sm.fail;
+    const int g = lane >> 2, c = lane & 3;
+    // place of this lane's eight bytes of step s, entry n = 8 nt + g of chunk w: block s / 4, row 16 w + n
+    uint32_t at[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) at[q] = (16 * w + g) * 128 + ((((c >> 1) ^ g) ^ (2 * q)) << 4) + 8 * (c & 1);
+    Query qy;
+    int T = 0, seg = 0;
+    for (; wk.left > 0; wk.next(P), ++seg) {
+        qy.load(P, wk.b, wk.rq, g, c);
+        const int p = wk.s.n - P.Q + wk.rq / P.groups;   // the query's position
+        float nm[2] = {kUnset, kUnset}, l[2] = {0.f, 0.f}, gs = 0.f;   // gs = 0: g not set yet
+        for (int t = 0; t < wk.len; ++t, ++T) {
+            const int st = T % kStages, buf = T & 1;
+            bool ok = wait(&sm.full[st], (T / kStages) & 1, fail);
+            if (T >= 2) ok = ok && wait(&sm.pempty[buf], ((T >> 1) - 1) & 1, fail);
+            ok = __all_sync(0xffffffffu, ok);
+            const int tok0 = ok ? sm.chunk_tok[st][w] : -1;
+            auto sees_entry = [&](int en) { return tok0 >= 0 && sees(P, tok0 + en, p); };
+            float acc[2][2][4], racc[2][4];   // [entries 8 nt ..][half of a step: independent chains], RoPE part
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[nt][0][i] = acc[nt][1][i] = racc[nt][i] = 0.f;
+            uint8_t* img = kFp4 ? sm.img[kFp4 ? buf : 0] : sm.stage[st];
+            float fe[2][2];   // of the entries 8 nt + 2 c + i: the columns of this lane's scores
+            if constexpr (kFp4) {
+                const uint8_t* ch = sm.stage[st] + w * kChunk4Bytes;
+                // RoPE rows into the image, eight lanes a row
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int en = 4 * i + (lane >> 3), k = lane & 7;
+                    uint4 v = *reinterpret_cast<const uint4*>(ch + kChunk4Rope + en * 2 * kRope + 16 * k);
+                    if (!sees_entry(en)) v = make_uint4(0, 0, 0, 0);
+                    *reinterpret_cast<uint4*>(img + 4 * kBlkBytes + sw128(16 * w + en, 16 * k)) = v;
+                }
+                int base[2];
+                uint32_t tx[2], ty[2], dx[2], dy[2];
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt) {
+                    const bool vis = sees_entry(8 * nt + g);   // masked: every byte decodes to a signed zero
+                    base[nt] = ch[kChunk4Exp + kGroups * kChunk + 8 * nt + g];
+                    tx[nt] = vis ? kTabX : 0u;
+                    ty[nt] = vis ? kTabY : 0u;
+                    dx[nt] = vis ? kTabDx : 0u;
+                    dy[nt] = vis ? kTabDy : 0u;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t eb = ch[kChunk4Exp + kGroups * kChunk + 8 * nt + 2 * c + i];
+                        fe[nt][i] = __uint_as_float(eb << 23) * 0x1p-13f;
+                    }
+                }
+                // j above kMaxJ (a group of 2^-26 of the entry's largest: zero) or below 0 (a NaN group) in some entry.
+                // Lane (g, c) looks at the groups c, c + 4, ..
+                uint32_t most = 0;
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                    for (int s = 0; s < 4; ++s)
+                        if (dx[nt] && 4 * s + c < kSteps)
+                            most = max(most, static_cast<uint32_t>(base[nt] - ch[kChunk4Exp + (4 * s + c) * kChunk + 8 * nt + g]));
+                const bool far = __any_sync(0xffffffffu, most > kMaxJ);
+                // words and exponents come in blocks of four steps, a block ahead of their use (a load may not pass a
+                // store to the image, as far as the compiler knows)
+                uint32_t wd[2][4][2];
+                int ex[2][4][2];
+                auto fetch = [&](int blk) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int nt = 0; nt < 2; ++nt) {
+                            const int s = 4 * blk + i;
+                            if (s >= kSteps) continue;
+                            wd[blk & 1][i][nt] = *reinterpret_cast<const uint32_t*>(ch + s * 256 + (8 * nt + g) * 16 + 4 * c);
+                            ex[blk & 1][i][nt] = ch[kChunk4Exp + s * kChunk + 8 * nt + g];
+                        }
+                };
+                fetch(0);
+#pragma unroll
+                for (int blk = 0; blk < 4; ++blk) {
+                    if (blk < 3) fetch(blk + 1);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int nt = 0; nt < 2; ++nt) {
+                            const int s = 4 * blk + i;
+                            if (s >= kSteps) continue;
+                            const int j = base[nt] - ex[blk & 1][i][nt];
+                            uint2 tab = make_uint2(tx[nt] - j * dx[nt], ty[nt] - j * dy[nt]);
+                            if (far && dx[nt] && (j < 0 || j > kMaxJ)) tab.x = tab.y = j < 0 ? 0x7F7F7F7Fu : 0u;
+                            uint32_t b0, b1;
+                            decode8(wd[blk & 1][i][nt], tab, b0, b1);
+                            *reinterpret_cast<uint2*>(img + blk * kBlkBytes + nt * 1024 + at[i]) = make_uint2(b0, b1);
+                            mma_f16(acc[nt][0], qy.f[s][0], bytes_to_f16x2<true, 0>(b0), bytes_to_f16x2<true, 1>(b0));
+                            mma_f16(acc[nt][1], qy.f[s][1], bytes_to_f16x2<true, 0>(b1), bytes_to_f16x2<true, 1>(b1));
+                        }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.empty[st]);
+            } else {
+                fe[0][0] = fe[0][1] = fe[1][0] = fe[1][1] = 1.f;
+                // masked rows are zeroed for the value warps
+                if (!__all_sync(0xffffffffu, sees_entry(lane & 15))) {
+                    for (int en = 0; en < 16; ++en)
+                        if (!sees_entry(en))
+                            for (int k = lane; k < 40; k += 32)
+                                *reinterpret_cast<uint4*>(img + (k >> 3) * kBlkBytes + sw128(16 * w + en, 16 * (k & 7))) = make_uint4(0, 0, 0, 0);
+                    fence_proxy_async_smem();   // the ring's next copy writes there too
+                    __syncwarp();
+                }
+#pragma unroll
+                for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+                    for (int nt = 0; nt < 2; ++nt) {
+                        const uint2 b = *reinterpret_cast<const uint2*>(img + (s >> 2) * kBlkBytes + nt * 1024 + at[s & 3]);
+                        mma_f16(acc[nt][0], qy.f[s][0], bytes_to_f16x2<false, 0>(b.x), bytes_to_f16x2<false, 1>(b.x));
+                        mma_f16(acc[nt][1], qy.f[s][1], bytes_to_f16x2<false, 0>(b.y), bytes_to_f16x2<false, 1>(b.y));
+                    }
+            }
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt) {
+                    const uint2 b = *reinterpret_cast<const uint2*>(img + 4 * kBlkBytes + nt * 1024 + at[s]);
+                    mma_bf16(racc[nt], qy.rope[s][0], qy.rope[s][1], qy.rope[s][2], qy.rope[s][3], b.x, b.y);
+                }
+            // logits x[nt][2 r + i]: entry 8 nt + 2 c + i, head g + 8 r (log2 units), -inf where masked
+            float x[2][4];
+            bool see[2][2];
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    see[nt][i] = sees_entry(8 * nt + 2 * c + i);
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const int k = 2 * r + i;
+                        const float v = kFp4 ? fmaf(acc[nt][0][k] + acc[nt][1][k], fe[nt][i], racc[nt][k])
+                                             : (acc[nt][0][k] + acc[nt][1][k]) + racc[nt][k];
+                        x[nt][k] = see[nt][i] ? v * qy.c2[r] : -INFINITY;
+                    }
+                    if (!see[nt][i]) fe[nt][i] = 0.f;
+                }
+            float top[2], fmost = fmaxf(fmaxf(fe[0][0], fe[0][1]), fmaxf(fe[1][0], fe[1][1]));
+#pragma unroll
+            for (int r = 0; r < 2; ++r) top[r] = fmaxf(fmaxf(x[0][2 * r], x[0][2 * r + 1]), fmaxf(x[1][2 * r], x[1][2 * r + 1]));
+            const bool over = top[0] + nm[0] > kOver<kFp4> || top[1] + nm[1] > kOver<kFp4> || (kFp4 && fmost * gs > kFeMost);
+            int resc = t == 0 ? 2 : 0;
+            if (named_barrier_or(kBarScore, 32 * kScoreWarps, over)) {
+                // some weight is too large, or the first tile: the tile's maxima; a head that lies more than 2 above its
+                // mark gets a new one, and the value warps the factors of what they hold
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
+                    top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
+                    if (c == 0) sm.tmax[w][g + 8 * r] = top[r];
+                }
+                if constexpr (kFp4) {
+                    const uint32_t fm = __reduce_max_sync(0xffffffffu, __float_as_uint(fmost));
+                    if (lane == 0) sm.femax[w] = __uint_as_float(fm);
+                }
+                named_barrier(kBarScore, 32 * kScoreWarps);
+                float fg = 1.f;
+                if constexpr (kFp4) {
+                    const float fm = fmaxf(fmaxf(sm.femax[0], sm.femax[1]), fmaxf(sm.femax[2], sm.femax[3]));
+                    if (fm > 0.f && (gs == 0.f || fm * gs > kFeMost)) {
+                        const float gn = kFeSet / fmaxf(fm, 0x1p-110f);
+                        if (gs != 0.f) fg = gn / gs;
+                        gs = gn;
+                    }
+                }
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    float tm = sm.tmax[0][g + 8 * r];
+#pragma unroll
+                    for (int k = 1; k < kScoreWarps; ++k) tm = fmaxf(tm, sm.tmax[k][g + 8 * r]);
+                    const bool first = nm[r] == kUnset;
+                    const bool set = first ? tm > -INFINITY : tm + nm[r] > kLift<kFp4> + 2.f;
+                    const float to = set ? kLift<kFp4> - tm : nm[r];
+                    const float f = set && !first ? exp2_ftz(to - nm[r]) : 1.f;
+                    l[r] *= f;
+                    nm[r] = to;
+                    if (w == 0 && c == 0) {
+                        sm.fn[buf][g + 8 * r] = f * fg;
+                        sm.fr[buf][g + 8 * r] = f;
+                    }
+                }
+                if (t > 0) resc = 1;
+            }
+            // P: p = 2^(x + nm), as A fragments: of the chunk's 16 entries a lane holds 8 nt + 2 c + i, the MMA's k slots
+            // 2c + i (nt = 0) and 2c + 8 + i
+            uint32_t pb[2][2], ph[2][2];   // [r][nt]
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt) {
+                    const float p0 = exp2_ftz(x[nt][2 * r] + nm[r]), p1 = exp2_ftz(x[nt][2 * r + 1] + nm[r]);
+                    l[r] += p0 + p1;
+                    pb[r][nt] = f32x2_to_bf16x2_bits(p0, p1);
+                    ph[r][nt] = kFp4 ? f32x2_to_f16x2(p0 * (fe[nt][0] * gs), p1 * (fe[nt][1] * gs)) : f32x2_to_f16x2(p0, p1);
+                }
+            sm.p16[buf][w][lane] = make_uint4(ph[0][0], ph[1][0], ph[0][1], ph[1][1]);
+            sm.pbf[buf][w][lane] = make_uint4(pb[0][0], pb[1][0], pb[0][1], pb[1][1]);
+            if (w == 0 && lane == 0) sm.resc[buf] = resc;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.pfull[buf]);
+        }
+        // ---- the segment's sums --------------------------------------------------------------------
+        const int sb = seg & 1;
+        if (seg >= 2) (void)wait(&sm.segempty[sb], ((seg >> 1) - 1) & 1, fail);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+            if (c == 0) {
+                sm.lsum[sb][w][g + 8 * r] = l[r];
+                if (w == 0) sm.mseg[sb][g + 8 * r] = -nm[r];
+            }
+        }
+        if (w == 0 && lane == 0) {
+            sm.ginv[sb] = gs != 0.f ? 1.f / gs : 1.f;
+            if (wk.t == 0 && wk.len < wk.s.tiles) {   // a cut row begins here: which CTA holds its end
+                const int64_t row = (int64_t)wk.b * P.Q * P.groups + wk.rq;
+                const int64_t end = u1 - wk.left + wk.s.tiles;    // unit behind the row
+                int64_t e = (end - 1) * n_cta / total;
+                while (total * (e + 1) / n_cta <= end - 1) ++e;
+                while (total * e / n_cta > end - 1) --e;
+                P.meta[blockIdx.x] = make_int4(static_cast<int>(row), static_cast<int>(row >> 32), static_cast<int>(e), 0);
+            }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.segfull[sb]);
+    }
+}
+
+// ---- value warps ---------------------------------------------------------------------------------
 template <bool kFp4>
-struct IssuePv {
-    Smem<kFp4>& sm;
-    uint32_t acc0;
-    template <int kSt, int kBuf> __device__ __forceinline__ void operator()() { issue_pv<kFp4, kSt, kBuf>(sm, acc0); }
-};
+__device__ __forceinline__ void value_role(Smem<kFp4>& sm, const Params& P, Walk wk, int w, int lane) {
+    constexpr int kStages = Smem<kFp4>::kStages;
+    volatile int32_t* fail = &sm.fail;
+    const int g = lane >> 2, c = lane & 3;
+    const bool rope = w == kValueWarps - 1;
+    // this lane's row address of the matrix loads within a 32-entry block (448 dims) or a 16-entry chunk (RoPE), and
+    // the 16-byte column it starts from
+    int row, col;
+    if (!rope) {
+        const int k = lane & 15, i = k & 3;   // row k of a transposing load (slots 4c + i) -> entry of the chunk lane / 16
+        row = 16 * (lane >> 4) + (i < 2 ? 2 * (k >> 2) + i : 8 + 2 * (k >> 2) + i - 2);
+        col = 4 * (w & 1);
+    } else {
+        row = (lane & 7) + 8 * ((lane >> 3) & 1);
+        col = lane >> 4;
+    }
+    const uint32_t off = (rope ? 4 : w >> 1) * kBlkBytes + (row >> 3) * 1024 + (row & 7) * 128;
+    float o[8][4];
+    int T = 0, seg = 0;
+    for (; wk.left > 0; wk.next(P), ++seg) {
+        for (int t = 0; t < wk.len; ++t, ++T) {
+            const int buf = T & 1, st = T % kStages;
+            bool ok = wait(&sm.pfull[buf], (T >> 1) & 1, fail);
+            if (!kFp4) ok = ok && wait(&sm.full[st], (T / kStages) & 1, fail);   // complete: makes the copy visible here
+            ok = __all_sync(0xffffffffu, ok);
+            const int resc = sm.resc[buf];
+            if (resc == 2) {
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[q][i] = 0.f;
+            } else if (resc == 1) {
+                const float* f = rope ? sm.fr[buf] : sm.fn[buf];
+                const float f0 = f[g], f1 = f[g + 8];
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    o[q][0] *= f0;
+                    o[q][1] *= f0;
+                    o[q][2] *= f1;
+                    o[q][3] *= f1;
+                }
+            }
+            if (ok) {
+                const uint32_t base = smem_u32(kFp4 ? sm.img[kFp4 ? buf : 0] : sm.stage[st]) + off;
+                if (!rope) {
+#pragma unroll
+                    for (int kb = 0; kb < kTile / 32; ++kb) {
+                        const uint4 p0 = sm.p16[buf][2 * kb][lane], p1 = sm.p16[buf][2 * kb + 1][lane];
+                        const uint32_t a0[4] = {p0.x, p0.y, p0.z, p0.w}, a1[4] = {p1.x, p1.y, p1.z, p1.w};
+                        uint32_t v[4][4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) ldmatrix_b8_trans_x2(v[q], base + kb * 4096 + (((col + q) ^ (row & 7)) << 4));
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            mma_f16(o[2 * q], a0, bytes_to_f16x2<kFp4, 0>(v[q][0]), bytes_to_f16x2<kFp4, 1>(v[q][0]));
+                            mma_f16(o[2 * q + 1], a0, bytes_to_f16x2<kFp4, 0>(v[q][1]), bytes_to_f16x2<kFp4, 1>(v[q][1]));
+                        }
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            mma_f16(o[2 * q], a1, bytes_to_f16x2<kFp4, 0>(v[q][2]), bytes_to_f16x2<kFp4, 1>(v[q][2]));
+                            mma_f16(o[2 * q + 1], a1, bytes_to_f16x2<kFp4, 0>(v[q][3]), bytes_to_f16x2<kFp4, 1>(v[q][3]));
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < kTileChunks; ++k) {
+                        const uint4 a = sm.pbf[buf][k][lane];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            uint32_t v[4];
+                            ldmatrix_b16_trans_x4(v, base + k * 2048 + (((col + 2 * q) ^ (row & 7)) << 4));
+                            mma_bf16(o[2 * q], a.x, a.y, a.z, a.w, v[0], v[1]);
+                            mma_bf16(o[2 * q + 1], a.x, a.y, a.z, a.w, v[2], v[3]);
+                        }
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&sm.pempty[buf]);
+                if (!kFp4) mbar_arrive(&sm.empty[st]);
+            }
+        }
+        // ---- the segment's result ------------------------------------------------------------------
+        const int sb = seg & 1;
+        const bool ok = __all_sync(0xffffffffu, wait(&sm.segfull[sb], (seg >> 1) & 1, fail));
+        float L[2], M[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int h = g + 8 * r;
+            L[r] = (sm.lsum[sb][0][h] + sm.lsum[sb][1][h]) + (sm.lsum[sb][2][h] + sm.lsum[sb][3][h]);
+            M[r] = sm.mseg[sb][h];
+        }
+        const float gi = rope ? 1.f : sm.ginv[sb];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.segempty[sb]);
+        if (!ok) continue;
+        const bool whole = wk.t == 0 && wk.len == wk.s.tiles;
+        const int j = wk.rq / P.groups, h0 = 16 * (wk.rq % P.groups) + g;
+        const int64_t head = ((int64_t)wk.b * P.Q + j) * P.heads + h0;
+        const int64_t slot = 2 * (int64_t)blockIdx.x + (wk.t == 0 ? 1 : 0);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const float f = whole ? (L[r] == 0.f ? 0.f : gi / L[r]) : gi;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                const int d = 64 * w + 8 * q + 2 * c;
+                const float v0 = o[q][2 * r] * f, v1 = o[q][2 * r + 1] * f;
+                if (!whole) *reinterpret_cast<float2*>(P.opart + (slot * kHeads + g + 8 * r) * kDim + d) = make_float2(v0, v1);
+                else if (h0 + 8 * r < P.heads) store_out2(P, (head + 8 * r) * kDim + d, v0, v1);
+            }
+            if (w == 0 && c == 0) {
+                if (!whole) P.mlpart[slot * kHeads + g + 8 * r] = make_float2(M[r], L[r]);
+                else if (P.lse && h0 + 8 * r < P.heads)
+                    P.lse[head + 8 * r] = L[r] == 0.f ? -INFINITY : (M[r] + log2f(L[r])) * 0.69314718055994531f;
+            }
+        }
+    }
+}
+
+// ---- copy warp -------------------------------------------------------------------------------------
+template <bool kFp4>
+__device__ __forceinline__ void copy_role(Smem<kFp4>& sm, const Params& P, Walk wk, int lane, const CUtensorMap* pages_map) {
+    constexpr int kStages = Smem<kFp4>::kStages;
+    volatile int32_t* fail = &sm.fail;
+    int T = 0;
+    // lane i < 4: chunk i of the tile; its first token and page, loaded one tile ahead
+    auto look = [&](const Walk& w, int t, int& tok, int32_t& pg) {
+        tok = lane < kTileChunks ? w.token_of_chunk((w.t + t) * kTileChunks + lane) : -1;
+        pg = tok >= 0 ? __ldg(P.c.table + (int64_t)w.b * P.c.max_pages + tok / P.c.page_size) : -1;
+    };
+    for (; wk.left > 0; wk.next(P)) {
+        int tok, tok1 = -1;
+        int32_t pg, pg1 = -1;
+        look(wk, 0, tok, pg);
+        for (int t = 0; t < wk.len; ++t, ++T) {
+            if (t + 1 < wk.len) look(wk, t + 1, tok1, pg1);
+            const int st = T % kStages;
+            bool ok = !*fail;
+            if (T >= kStages) ok = ok && wait(&sm.empty[st], (T / kStages - 1) & 1, fail);
+            if (!__all_sync(0xffffffffu, ok)) return;
+            if (tok >= 0 && (pg < 0 || pg >= P.c.n_pages)) {
+                dev_error(P.err, CSLD_DEVERR_PAGE);
+                tok = -1;
+            }
+            if (lane < kTileChunks) sm.chunk_tok[st][lane] = tok;
+            const int n = __popc(__ballot_sync(0xffffffffu, tok >= 0));
+            __syncwarp();
+            if (lane == 0) {
+                sm.n_issued = T + 1;
+                mbar_arrive_expect_tx(&sm.full[st], n * kChunk * (kFp4 ? kEntry4 : 5 * 128));
+            }
+            __syncwarp();
+            const int64_t row = (int64_t)pg * P.c.page_size + (tok >= 0 ? tok % P.c.page_size : 0);
+            if constexpr (kFp4) {
+                if (tok >= 0) bulk_g2s(sm.stage[st] + lane * kChunk4Bytes, P.c.pages + row * kEntry4, kChunk4Bytes, &sm.full[st]);
+            } else {
+                const int ck = lane / 5, blk = lane % 5;   // one box of 16 rows by 128 bytes a lane
+                const int tk = __shfl_sync(0xffffffffu, tok, ck < kTileChunks ? ck : 0);
+                const int y = __shfl_sync(0xffffffffu, static_cast<int>(row), ck < kTileChunks ? ck : 0);
+                if (ck < kTileChunks && tk >= 0)
+                    tma_load_2d(sm.stage[st] + blk * kBlkBytes + ck * kChunk * 128, pages_map, blk < 4 ? 128 * blk : kNope, y, &sm.full[st]);
+            }
+            tok = tok1;
+            pg = pg1;
+        }
+    }
+}
 
 }  // namespace
 
@@ -392,47 +706,27 @@ template <bool kFp4>
 __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __grid_constant__ CUtensorMap pages_map,
                                                                       const __grid_constant__ Params P) {
     using S = Smem<kFp4>;
-    constexpr int kBufs = S::kBufs;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     S& sm = *reinterpret_cast<S*>(smem_raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
     // ---- setup --------------------------------------------------------------------------------
     if (tid == 0) {
-        for (int s = 0; s < kBufs; ++s) {
-            mbar_init(&sm.stfull[s], 1);
-            mbar_init(&sm.imgfull[s], kConvWarps);
-            mbar_init(&sm.imgempty[s], 1);
+        for (int s = 0; s < S::kStages; ++s) {
+            mbar_init(&sm.full[s], 1);
+            mbar_init(&sm.empty[s], kFp4 ? kScoreWarps : kValueWarps);
         }
         for (int s = 0; s < 2; ++s) {
-            mbar_init(&sm.stempty[s], kConvWarps);
-            mbar_init(&sm.sfull[s], 1);
-            mbar_init(&sm.pfull[s], 8);
-            mbar_init(&sm.pdone[s], 1);
+            mbar_init(&sm.pfull[s], kScoreWarps);
+            mbar_init(&sm.pempty[s], kValueWarps);
+            mbar_init(&sm.segfull[s], kScoreWarps);
+            mbar_init(&sm.segempty[s], kValueWarps);
         }
-        mbar_init(&sm.qready, 16);
-        mbar_init(&sm.drain, 1);
         sm.fail = 0;
         sm.n_issued = 0;
         fence_barrier_init();
     }
-    if (warp == kMmaWarp) {
-        tmem_alloc(&sm.tmem_base, 512);
-        tmem_relinquish();
-    }
-    if (kFp4 && tid >= 512 && tid < 512 + kLutRows) {   // table rows: 2^(6-j) times the E2M1 grid in E4M3
-        const int j = tid - 513;
-        const float s = j < 0 ? __uint_as_float(0x7FC00000u) : j == kLutRows - 2 ? 0.f : pow2f(6 - j);
-        const float twice[8] = {0.f, 1.f, 2.f, 3.f, 4.f, 6.f, 8.f, 12.f};
-        uint32_t w[2] = {0u, 0u};
-#pragma unroll
-        for (int k = 0; k < 8; ++k) w[k >> 2] |= f32_to_e4m3(0.5f * twice[k] * s) << (8 * (k & 3));
-        sm.lut[tid - 512] = make_uint2(w[0], w[1]);
-    }
     if (!kFp4 && warp == kCopyWarp && lane == 0) tma_prefetch_map(&pages_map);
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
     pdl_wait();
     pdl_trigger();
 
@@ -444,8 +738,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
         if ((n < 0 || n > P.c.capacity()) && blockIdx.x == 0) dev_error(P.err, CSLD_DEVERR_SEQ_LEN);
         mine += seq_info(P, b).tiles;
     }
-    // tiles of all sequences, then (per batch of 768 sequences) the sequence that the share begins in
-    int64_t* red = reinterpret_cast<int64_t*>(sm.fe[0]);
     auto block_scan = [&](int64_t v, int64_t& total) {   // exclusive prefix of v over the threads
         int64_t inc = v;
 #pragma unroll
@@ -454,13 +746,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
             if (lane >= o) inc += y;
         }
         __syncthreads();
-        if (lane == 31) red[warp] = inc;
+        if (lane == 31) sm.red[warp] = inc;
         __syncthreads();
         int64_t before = 0;
         total = 0;
         for (int w = 0; w < kThreads / 32; ++w) {
-            if (w < warp) before += red[w];
-            total += red[w];
+            if (w < warp) before += sm.red[w];
+            total += sm.red[w];
         }
         return before + inc - v;
     };
@@ -471,7 +763,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
     const int64_t u0 = blockIdx.x < n_cta ? total * blockIdx.x / n_cta : 0;
     const int64_t u1 = blockIdx.x < n_cta ? total * (blockIdx.x + 1) / n_cta : 0;
     const int n_tiles = static_cast<int>(u1 - u0);
-    if (n_tiles > 0) {
+    if (n_tiles > 0) {   // the sequence that the share begins in
         int64_t base = 0;
         for (int b1 = 0; b1 < P.c.batch; b1 += kThreads) {
             int64_t v, p, tot;
@@ -490,413 +782,27 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
             base += tot;
         }
     }
+    if (tid == 0) P.meta[blockIdx.x] = make_int4(0, 0, -1, 0);   // overwritten by this thread where a cut row begins
     __syncthreads();
-    const uint32_t tmem = sm.tmem_base;
-    volatile int32_t* fail = &sm.fail;
-    if (tid == 0) P.meta[blockIdx.x] = make_int4(0, 0, -1, 0);   // its thread overwrites it below where a cut row begins
-
     if (n_tiles > 0) {
         Walk wk;
         wk.begin(P, sm.b0, u0 - sm.prefix, n_tiles);
-        if (warp < 16) {
-            // ===== softmax: stream = warp / 8, thread = entry e (TMEM lane), heads 8 hg .. 8 hg + 7 ===============
-            const int st = warp >> 3, hg = (warp >> 2) & 1, sub = warp & 3, e = 32 * sub + lane;
-            const uint32_t lb = tmem + ((32u * sub) << 16);
-            const uint32_t ts = lb + kColS + kStepS * st + 8u * hg, to = lb + kColO + kStepO * st + 8u * hg;
-            auto load_query = [&](uint4 (&v)[2]) {
-                const int j = wk.rq / P.groups, h = 16 * (wk.rq % P.groups) + warp;
-                v[0] = v[1] = make_uint4(0, 0, 0, 0);
-                if (h < P.heads) {
-                    const uint4* src = reinterpret_cast<const uint4*>(
-                        P.q + (((int64_t)wk.b * P.Q + j) * P.heads + h) * kDim + 16 * lane);
-                    v[0] = __ldg(src);
-                    v[1] = __ldg(src + 1);
-                }
-            };
-            int T = 0;   // running tile of the CTA; stream st takes those with T % 2 == st
-            for (; wk.left > 0; wk.next(P)) {
-                {
-                    uint4 v[2];
-                    load_query(v);
-                    prepare_query<kFp4>(sm, v, warp, lane, P.scale);
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.qready);
-                named_barrier(kBarAll, 512);   // c2 of every head
-                float nm[8], l[8], g = 0.f;   // nm = kUnset, g = 0: not set yet
-#pragma unroll
-                for (int h = 0; h < 8; ++h) {
-                    nm[h] = kUnset;
-                    l[h] = 0.f;
-                }
-                const int T1 = T + wk.len;
-                for (T += (T ^ st) & 1; T < T1; T += 2) {
-                    const int buf = kFp4 ? st : T % 3;
-                    bool ok = wait(&sm.imgfull[buf], (T / kBufs) & 1, fail);   // (for f_e) done before S is
-                    ok = ok && wait(&sm.sfull[st], (T >> 1) & 1, fail);
-                    ok = __all_sync(0xffffffffu, ok);
-                    tc_fence_after();
-                    float t[8], fe = -1.f;
-                    bool over = false;
-                    const float* c2 = sm.c2 + 8 * hg;
-                    // First try against the maximum as it stands (the common case): one meeting of the stream's
-                    // warps.  S(T) complete implies PV(T-2) complete, so P and O are free to be written.
-                    if (sub < kTile / 32) {
-                        fe = ok ? sm.fe[buf][e] : -1.f;
-                        load_t<kFp4>(t, ts, c2, nm, fe, fe >= 0.f);
-                        float top = t[0];
-#pragma unroll
-                        for (int h = 1; h < 8; ++h) top = fmaxf(top, t[h]);
-                        over = top > kOver<kFp4> || (kFp4 && fe * g > kFeMost);
-                        if (!__any_sync(0xffffffffu, over)) write_p<kFp4>(sm.p8[st], sm.pbf[st], t, fe >= 0.f ? fe * g : 0.f, hg, e);
-                    }
-                    fence_proxy_async_smem();
-                    if (named_barrier_or(kBarStream + st, 256, over)) {
-                        // some weight is too large, or the first tile: the tile's maxima (of the logits themselves, nm
-                        // may be unset), every head that lies more than 2 above its mark set anew, O rescaled
-                        const bool seen = fe >= 0.f;
-                        if (sub < kTile / 32) {
-                            float z[8];
-#pragma unroll
-                            for (int h = 0; h < 8; ++h) z[h] = 0.f;
-                            load_t<kFp4>(t, ts, c2, z, fe, seen);
-                            float mine = 0.f;
-#pragma unroll
-                            for (int h = 0; h < 8; ++h) {
-                                const float top = key_to_float(__reduce_max_sync(0xffffffffu, score_key(t[h])));
-                                mine = lane == h ? top : mine;
-                            }
-                            if (lane < 8) sm.tmax[st][sub][8 * hg + lane] = mine;
-                            if (kFp4 && hg == 0) {
-                                const uint32_t fm = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(fe, 0.f)));
-                                if (lane == 0) sm.femax[st][sub] = __uint_as_float(fm);
-                            }
-                        }
-                        named_barrier(kBarStream + st, 256);
-                        float f[8], fg = 1.f;
-                        bool rescale = false;
-                        if constexpr (kFp4) {
-                            const float fm = fmaxf(fmaxf(sm.femax[st][0], sm.femax[st][1]), sm.femax[st][2]);
-                            if (fm > 0.f && (g == 0.f || fm * g > kFeMost)) {
-                                const float gn = kFeSet / fmaxf(fm, 0x1p-110f);
-                                if (g != 0.f) {
-                                    fg = gn / g;
-                                    rescale = true;
-                                }
-                                g = gn;
-                            }
-                        }
-#pragma unroll
-                        for (int h = 0; h < 8; ++h) {
-                            float tm = sm.tmax[st][0][8 * hg + h];
-#pragma unroll
-                            for (int q3 = 1; q3 < kTile / 32; ++q3) tm = fmaxf(tm, sm.tmax[st][q3][8 * hg + h]);
-                            const bool first = nm[h] == kUnset;
-                            const bool set = first ? tm > -INFINITY : tm + nm[h] > kLift<kFp4> + 2.f;
-                            const float to_nm = set ? kLift<kFp4> - tm : nm[h];
-                            f[h] = set && !first ? exp2_ftz(to_nm - nm[h]) : 1.f;
-                            rescale |= set && !first;
-                            l[h] *= f[h];
-                            nm[h] = to_nm;
-                        }
-                        if (rescale) {   // the same answer in every thread of the head group
-#pragma unroll 2
-                            for (int c = 0; c < 13; ++c) {   // 4 blocks of 3 terms, then RoPE
-                                uint32_t o[8];
-                                const float fc = c < 12 ? fg : 1.f;
-                                tmem_ld_32x32b_x8(to + 16u * c, o);
-                                tmem_ld_wait();
-#pragma unroll
-                                for (int h = 0; h < 8; ++h) o[h] = __float_as_uint(__uint_as_float(o[h]) * (f[h] * fc));
-                                tmem_st_32x32b_x8(to + 16u * c, o);
-                            }
-                            tmem_st_wait();
-                        }
-                        if (sub < kTile / 32) {
-#pragma unroll
-                            for (int h = 0; h < 8; ++h) t[h] += nm[h];
-                            write_p<kFp4>(sm.p8[st], sm.pbf[st], t, seen ? fe * g : 0.f, hg, e);
-                        }
-                        fence_proxy_async_smem();
-                        named_barrier(kBarStream + st, 256);
-                    }
-                    if (sub < kTile / 32) {
-#pragma unroll
-                        for (int h = 0; h < 8; ++h) l[h] += t[h];
-                    }
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sm.pfull[st]);
-                }
-                const int T_last = T - 2;   // the stream's last tile so far (any segment)
-                T = T1;
-                const bool had = T_last >= T1 - wk.len;   // the stream had a tile of this segment
-                if (had) (void)wait(&sm.pdone[st], (T_last >> 1) & 1, fail);
-                // ---- the segment's result: sums over the lane quarters, then both streams joined -------------
-#pragma unroll
-                for (int h = 0; h < 8; ++h) {
-#pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], o);
-                    if (lane == h) sm.tmax[st][sub][8 * hg + h] = l[h];
-                }
-                named_barrier(kBarStream + st, 256);
-                if (sub == 0 && lane < 8) {
-                    const int hh = 8 * hg + lane;
-                    float mm = nm[0];
-#pragma unroll
-                    for (int h = 1; h < 8; ++h) mm = lane == h ? nm[h] : mm;
-                    if (hh == 0) sm.ginv[st] = g != 0.f ? 1.f / g : 1.f;
-                    sm.ml[st][hh] = make_float2(-mm, (sm.tmax[st][0][hh] + sm.tmax[st][1][hh]) + (sm.tmax[st][2][hh] + sm.tmax[st][3][hh]));
-                }
-                tc_fence_before();
-                named_barrier(kBarAll, 512);
-                tc_fence_after();
-                // l == 0: the stream saw nothing (its O may be stale); a NaN sum is no zero
-                float a0[8], a1[8], M[8], L[8];
-                bool use0 = false, use1 = false;
-#pragma unroll
-                for (int h = 0; h < 8; ++h) {
-                    const float2 s0 = sm.ml[0][8 * hg + h], s1 = sm.ml[1][8 * hg + h];
-                    const bool z0 = s0.y == 0.f, z1 = s1.y == 0.f;
-                    M[h] = z0 ? (z1 ? -INFINITY : s1.x) : (z1 ? s0.x : fmaxf(s0.x, s1.x));
-                    a0[h] = z0 ? 0.f : exp2_ftz(s0.x - M[h]);
-                    a1[h] = z1 ? 0.f : exp2_ftz(s1.x - M[h]);
-                    L[h] = a0[h] * s0.y + a1[h] * s1.y;
-                    use0 |= !z0;
-                    use1 |= !z1;
-                }
-                const bool whole = wk.t == 0 && wk.len == wk.s.tiles;
-                const int j = wk.rq / P.groups, h0 = 16 * (wk.rq % P.groups) + 8 * hg;
-                const int64_t at = ((int64_t)wk.b * P.Q + j) * P.heads + h0;
-                const int64_t slot = 2 * (int64_t)blockIdx.x + (wk.t == 0 ? 1 : 0);
-                if (!*fail) {
-                    // stream 0's warps write dims 0..255, stream 1's the rest
-                    float inv[8];
-#pragma unroll
-                    for (int h = 0; h < 8; ++h) inv[h] = whole ? (L[h] == 0.f ? 0.f : 1.f / L[h]) : 1.f;
-                    const uint32_t o0 = lb + kColO + 8u * hg;
-                    const float gi[2] = {sm.ginv[0], sm.ginv[1]};
-#pragma unroll 1
-                    for (int c = 2 * st; c < 2 + 3 * st; ++c) {
-                        const bool rope = c == 4;
-                        float v[8];
-#pragma unroll
-                        for (int h = 0; h < 8; ++h) v[h] = 0.f;
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            if (!(k ? use1 : use0)) continue;   // uniform in the warp
-#pragma unroll 1
-                            for (int n = 0; n < (rope ? 1 : 3); ++n) {
-                                uint32_t o[8];
-                                tmem_ld_32x32b_x8(o0 + kStepO * k + 48u * c + 16u * n, o);
-                                tmem_ld_wait();
-#pragma unroll
-                                for (int h = 0; h < 8; ++h) {
-                                    const float a = (k ? a1[h] : a0[h]) * (rope ? 1.f : gi[k]);
-                                    if (a != 0.f) v[h] = fmaf(a, __uint_as_float(o[h]), v[h]);
-                                }
-                            }
-                        }
-                        const int d = rope ? kNope + e : 128 * c + e;
-                        if (rope ? e < kRope : d < kNope) {
-#pragma unroll
-                            for (int h = 0; h < 8; ++h) {
-                                if (whole) {
-                                    if (h0 + h < P.heads) store_out(P, (at + h) * kDim + d, v[h] * inv[h]);
-                                } else {
-                                    P.opart[(slot * kHeads + 8 * hg + h) * kDim + d] = v[h];
-                                }
-                            }
-                        }
-                    }
-                    if (st == 0 && sub == 0 && lane < 8) {
-                        float mm = M[0], ll = L[0];
-#pragma unroll
-                        for (int h = 1; h < 8; ++h) {
-                            mm = lane == h ? M[h] : mm;
-                            ll = lane == h ? L[h] : ll;
-                        }
-                        if (!whole) P.mlpart[slot * kHeads + 8 * hg + lane] = make_float2(mm, ll);
-                        else if (P.lse && h0 + lane < P.heads)
-                            P.lse[at + lane] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.69314718055994531f;
-                    }
-                    if (tid == 0 && wk.t == 0 && wk.len < wk.s.tiles) {   // a cut row begins here: its last CTA
-                        const int64_t row = (int64_t)wk.b * rows_per_seq + wk.rq;
-                        const int64_t end = u1 - wk.left + wk.s.tiles;    // unit behind the row
-                        int64_t c = (end - 1) * n_cta / total;
-                        while (total * (c + 1) / n_cta <= end - 1) ++c;
-                        while (total * c / n_cta > end - 1) --c;
-                        P.meta[blockIdx.x] = make_int4(static_cast<int>(row), static_cast<int>(row >> 32), static_cast<int>(c), 0);
-                    }
-                }
-                tc_fence_before();
-                named_barrier(kBarAll, 512);   // O, c2 and the query operands are free for the next row
-                tc_fence_after();
-            }
-        } else if (warp < kConvWarp + kConvWarps) {
-            // ===== convert ==================================================================================
-            const int ct = tid - 32 * kConvWarp, e = ct % kTile, part = ct / kTile;   // part: groups part, part + 4, ..
-            int T = 0;
-            for (; wk.left > 0; wk.next(P)) {
-                const int p = wk.s.n - P.Q + wk.rq / P.groups;   // the query's position
-                for (int t = 0; t < wk.len; ++t, ++T) {
-                    const int buf = T % kBufs;
-                    bool ok = wait(&sm.stfull[buf], (T / kBufs) & 1, fail);
-                    if (kFp4 && T >= kBufs) ok = ok && wait(&sm.imgempty[buf], (T / kBufs - 1) & 1, fail);
-                    ok = __all_sync(0xffffffffu, ok);
-                    uint8_t* img = sm.img[buf];
-                    const int ck = e / kChunk, tk = e % kChunk;
-                    auto seen = [&](int en) {
-                        const int c0 = sm.chunk_tok[buf][en / kChunk];
-                        return c0 >= 0 && sees(P, c0 + en % kChunk, p);
-                    };
-                    const bool vis = ok && seen(e);
-                    if constexpr (kFp4) {
-                        const uint8_t* ch = sm.stage[buf] + ck * kChunk4Bytes;
-                        const int ex0 = ch[kChunk4Exp + kGroups * kChunk + tk];
-                        if (part == 0) sm.fe[buf][e] = vis ? ldexpf(1.f, ex0 - 133) : -1.f;
-                        const int base = vis ? ex0 : 4096;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int g = part + 4 * i;
-                            if (g >= kGroups) break;   // whole warps
-                            const uint4 w = *reinterpret_cast<const uint4*>(ch + g * 256 + tk * 16);
-                            const int ex = ch[kChunk4Exp + g * kChunk + tk];   // 255 (NaN) is above every base
-                            const uint2 tab = sm.lut[1 + max(-1, min(base - ex, kLutRows - 2))];
-                            uint4 a, b;
-                            decode8(w.x, tab, a.x, a.y);
-                            decode8(w.y, tab, a.z, a.w);
-                            decode8(w.z, tab, b.x, b.y);
-                            decode8(w.w, tab, b.z, b.w);
-                            uint8_t* dst = img + i * kBlkBytes;
-                            *reinterpret_cast<uint4*>(dst + sw128(e, 32 * part)) = a;
-                            *reinterpret_cast<uint4*>(dst + sw128(e, 32 * part + 16)) = b;
-                        }
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {   // RoPE rows, eight threads per entry (no bank conflicts)
-                            const int en = (ct >> 3) + 48 * i, c = ct & 7;
-                            uint4 w = *reinterpret_cast<const uint4*>(sm.stage[buf] + (en / kChunk) * kChunk4Bytes + kChunk4Rope +
-                                                                      (en % kChunk) * 2 * kRope + 16 * c);
-                            if (!(ok && seen(en))) w = make_uint4(0, 0, 0, 0);
-                            *reinterpret_cast<uint4*>(img + kRopeBlk * kBlkBytes + sw128(en, 16 * c)) = w;
-                        }
-                    } else {
-                        if (part == 0) sm.fe[buf][e] = vis ? 1.f : -1.f;
-                        if (!vis && ok) {
-                            for (int c = part; c < 40; c += 4)
-                                *reinterpret_cast<uint4*>(img + (c >> 3) * kBlkBytes + sw128(e, 16 * (c & 7))) = make_uint4(0, 0, 0, 0);
-                        }
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(&sm.imgfull[buf]);
-                        if (kFp4) mbar_arrive(&sm.stempty[buf]);
-                    }
-                }
-            }
-        } else if (warp == kCopyWarp) {
-            // ===== copy ====================================================================================
-            int T = 0;
-            // lane i < 6: chunk i of the tile; its first token and page, loaded one tile ahead
-            auto look = [&](const Walk& w, int t, int& tok, int32_t& pg) {
-                tok = lane < kTileChunks && t < w.s.tiles ? w.token_of_chunk((w.t + t) * kTileChunks + lane) : -1;
-                pg = tok >= 0 ? __ldg(P.c.table + (int64_t)w.b * P.c.max_pages + tok / P.c.page_size) : -1;
-            };
-            for (; wk.left > 0; wk.next(P)) {
-                int tok, tok1 = -1;
-                int32_t pg, pg1 = -1;
-                look(wk, 0, tok, pg);
-                for (int t = 0; t < wk.len; ++t, ++T) {
-                    if (t + 1 < wk.len) look(wk, t + 1, tok1, pg1);
-                    const int buf = T % kBufs;
-                    bool ok = !*fail;
-                    if (T >= kBufs)
-                        ok = ok && wait(kFp4 ? &sm.stempty[buf & 1] : &sm.imgempty[buf], (T / kBufs - 1) & 1, fail);
-                    if (!__all_sync(0xffffffffu, ok)) break;
-                    if (tok >= 0 && (pg < 0 || pg >= P.c.n_pages)) {
-                        dev_error(P.err, CSLD_DEVERR_PAGE);
-                        tok = -1;
-                    }
-                    if (lane < kTileChunks) sm.chunk_tok[buf][lane] = tok;
-                    const int n = __popc(__ballot_sync(0xffffffffu, tok >= 0));
-                    if (lane == 0) mbar_arrive_expect_tx(&sm.stfull[buf], n * kChunk * (kFp4 ? kEntry4 : 5 * 128));
-                    __syncwarp();
-                    const int64_t row = (int64_t)pg * P.c.page_size + (tok >= 0 ? tok % P.c.page_size : 0);
-                    if constexpr (kFp4) {
-                        if (tok >= 0)
-                            bulk_g2s(sm.stage[buf] + lane * kChunk4Bytes, P.c.pages + row * kEntry4, kChunk4Bytes, &sm.stfull[buf]);
-                    } else {
-                        const int ck = lane / 5, blk = lane % 5;   // one box of 16 rows by 128 bytes per lane
-                        const int tk = __shfl_sync(0xffffffffu, tok, ck < kTileChunks ? ck : 0);
-                        const int y = __shfl_sync(0xffffffffu, static_cast<int>(row), ck < kTileChunks ? ck : 0);
-                        if (ck < kTileChunks && tk >= 0)
-                            tma_load_2d(sm.img[buf] + blk * kBlkBytes + ck * kChunk * 128, &pages_map, blk < 4 ? 128 * blk : kNope, y,
-                                        &sm.stfull[buf]);
-                    }
-                    tok = tok1;
-                    pg = pg1;
-                    if (lane == 0) sm.n_issued = T + 1;
-                }
-            }
-        } else if (lane == 0) {
-            // ===== MMA issue ==================================================================================
-            if (tmem != 0) *fail = 1;   // the MMAs' column constants
-            Walk wp = wk;                              // the walks of QK and of PV
-            int nq = 0, np = 0, qt = 0, pt = 0, seg = 0;   // running tiles, tiles within the segments
-            uint32_t idle = 0;
-            while (np < n_tiles) {
-                if (*fail) break;
-                if (np < nq && mbar_test(&sm.pfull[np & 1], (np >> 1) & 1)) {
-                    tc_fence_after();
-                    with_tile<kFp4>(np, IssuePv<kFp4>{sm, pt >= 2 ? 1u : 0u});   // a stream's first tile of a segment overwrites O
-                    ++np;
-                    if (++pt == wp.len) {
-                        pt = 0;
-                        wp.next(P);
-                    }
-                    idle = 0;
-                    continue;
-                }
-                if (nq < n_tiles && nq < np + 2 && mbar_test(&sm.imgfull[nq % kBufs], (nq / kBufs) & 1) &&
-                    (qt > 0 || mbar_test(&sm.qready, seg & 1))) {
-                    tc_fence_after();
-                    with_tile<kFp4>(nq, IssueQk<kFp4>{sm});
-                    ++nq;
-                    if (++qt == wk.len) {
-                        qt = 0;
-                        ++seg;
-                        wk.next(P);
-                    }
-                    idle = 0;
-                    continue;
-                }
-                if (++idle > (1u << 22)) {   // nothing became ready for about a second
-                    *fail = 1;
-                    break;
-                }
-                if (idle > 64) __nanosleep(20);
-            }
+        if (warp < kScoreWarps) {
+            regs_inc<kRegsScore>();
+            score_role<kFp4>(sm, P, wk, warp, lane, u1, n_cta, total);
+        } else if (warp < kValueWarp + kValueWarps) {
+            regs_dec<kRegsValue>();
+            value_role<kFp4>(sm, P, wk, warp - kValueWarp, lane);
+        } else {
+            regs_dec<kRegsCopy>();
+            if (warp == kCopyWarp) copy_role<kFp4>(sm, P, wk, lane, &pages_map);
         }
     }
-    tc_fence_before();
     __syncthreads();
-    if (sm.fail) {   // let the copies and MMAs in flight finish (bounded), then report
-        if (tid == 0) {
-            dev_error(P.err, CSLD_DEVERR_TIMEOUT);
-            const int n = sm.n_issued;
-            for (int T = max(0, n - kBufs); T < n; ++T) (void)mbar_wait(&sm.stfull[T % kBufs], (T / kBufs) & 1);
-        }
-        if (warp == kMmaWarp && lane == 0) {
-            umma_commit(&sm.drain);
-            (void)mbar_wait(&sm.drain, 0);
-        }
-        __syncthreads();
-    }
-    if (warp == kMmaWarp) {
-        tc_fence_after();
-        tmem_dealloc(tmem, 512);
+    if (sm.fail && tid == 0) {   // let the copies in flight finish (bounded), then report
+        dev_error(P.err, CSLD_DEVERR_TIMEOUT);
+        const int n = sm.n_issued;
+        for (int T = max(0, n - S::kStages); T < n; ++T) (void)mbar_wait(&sm.full[T % S::kStages], (T / S::kStages) & 1);
     }
 }
 
