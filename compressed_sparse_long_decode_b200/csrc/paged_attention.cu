@@ -52,41 +52,46 @@ namespace csld {
 
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kScoreWarps = 4, kValueWarp = 4, kValueWarps = 8, kCopyWarp = 12;
-// registers a thread: the launch gives 512 x 128 = 65,536; 128 x 216 + 256 x 120 + 128 x 40 = 63,488
-constexpr int kRegsScore = 216, kRegsValue = 120, kRegsCopy = 40;
-constexpr int kTile = 64, kTileChunks = kTile / kChunk;   // entries per tile; a chunk per score warp
-static_assert(kTileChunks == kScoreWarps, "score warp w takes chunk w");
+constexpr int kThreads = 640;
+constexpr int kGroupWarps = 4, kScoreWarps = 8, kValueWarp = 8, kValueWarps = 8, kCopyWarp = 16;
+// registers a thread: the launch gives 640 x 96 = 61,440 = 256 x 112 + 256 x 112 + 128 x 32
+constexpr int kRegsScore = 112, kRegsValue = 112, kRegsCopy = 32;
+constexpr int kTile = 64, kTileChunks = kTile / kChunk;   // entries per tile; a chunk per warp of a score group
+static_assert(kTileChunks == kGroupWarps, "a group's warp w takes chunk w");
 constexpr int kBlkBytes = kTile * 128;           // one 128-byte column block of a tile
 constexpr int kImgBytes = 5 * kBlkBytes;         // dims 0..127, 128..255, 256..383, 384..447, RoPE
 constexpr int kSteps = kGroups;                  // 32-dim steps of the 448 dims
+constexpr int kQSteps = 2 * kSteps + 4;          // 16-dim MMA steps of the query, the RoPE ones last
 // Marks: a head's nm is set so that the largest p of a tile is 2^kLift and kept until one exceeds 2^kOver.  The
 // operand holds p w in f16, w = 1 (fp8) or f_e g (fp4; g a power of two set so that the tile's largest f_e g is
 // kFeSet, kept until one exceeds kFeMost).  f16 bounds the product: 2^kOver w <= 2^15.
 template <bool kFp4> constexpr float kLift = kFp4 ? 0.f : 5.f;
 template <bool kFp4> constexpr float kOver = kFp4 ? 10.f : 15.f;
 constexpr float kFeSet = 8.f, kFeMost = 32.f, kUnset = 1e30f;
-constexpr int kBarScore = 1;                     // named barrier of the score warps
+constexpr int kBarGroup = 1, kBarScore = 3;      // named barriers: the score groups' (1, 2), both groups' (3)
 
-template <bool kFp4>
+template <bool kFp4, int R>
 struct Smem {
-    static constexpr int kStages = 5;
+    static constexpr int kStages = kFp4 && R == 1 ? 5 : 4;
     static constexpr int kStageBytes = kFp4 ? kTileChunks * kChunk4Bytes : kImgBytes;
     uint8_t img[kFp4 ? 2 : 1][kFp4 ? kImgBytes : 1024];   // fp4: value images [block][entry][128 B], 128-byte swizzle
     uint8_t stage[kStages][kStageBytes];         // fp8: the same layout, as copied
-    uint4 p16[2][kTileChunks][32];               // P in f16: [chunk][lane] A fragments
-    uint4 pbf[2][kTileChunks][32];               // bf16 P: [chunk][lane]
-    float fn[2][kHeads], fr[2][kHeads];          // factors of O before a tile's MMAs (448 dims; RoPE dims)
-    float tmax[kScoreWarps][kHeads], femax[kScoreWarps];
-    float lsum[2][kScoreWarps][kHeads], mseg[2][kHeads], ginv[2];   // a segment's sums, marks and 1 / g
-    int32_t chunk_tok[kStages][kTileChunks];     // first token of a tile's chunks; -1: none
+    uint4 qf[R][kQSteps][32];                    // the query's A fragments
+    uint4 p16[2][R][kTileChunks][32];            // P in f16: [chunk][lane] A fragments
+    uint4 pbf[2][R][kTileChunks][32];            // bf16 P
+    float fn[2][R][kHeads], fr[2][R][kHeads];    // factors of O before a tile's MMAs (448 dims; RoPE dims)
+    float c2[R][kHeads], sq[R][kHeads];          // logit factors (log2 units), scales of the query
+    float nm[R][kHeads], gs;                     // the marks
+    float tmax[2][kGroupWarps][R][kHeads], femax[2][kGroupWarps];
+    float lsum[2][kScoreWarps][R][kHeads], mseg[2][R][kHeads], ginv[2];   // a segment's sums, marks and 1 / g
+    int32_t chunk_tok[kStages][kTileChunks];           // first token of a tile's chunks; -1: none
     int32_t resc[2];                             // 0: O stays, 1: O *= f, 2: O = 0 (first tile of a segment)
-    uint64_t full[kStages], empty[kStages], pfull[2], pempty[2], segfull[2], segempty[2];
+    uint64_t full[kStages], empty[kStages], pfull[2], pempty[2], marked[2], segfull[2], segempty[2];
     int64_t red[kThreads / 32], prefix;
     int32_t fail, b0, n_issued;
 };
-static_assert(sizeof(Smem<true>) <= 232448 && sizeof(Smem<false>) <= 232448, "227 KB of shared memory");
+static_assert(sizeof(Smem<true, 1>) <= 232448 && sizeof(Smem<false, 1>) <= 232448, "227 KB of shared memory");
+static_assert(sizeof(Smem<true, 2>) <= 232448 && sizeof(Smem<false, 2>) <= 232448, "227 KB of shared memory");
 
 struct Params {
     PagedView c;
@@ -98,7 +103,7 @@ struct Params {
     int4* meta;          // [CTAs]: (row low, row high, last CTA, -) of the cut row that begins there; last CTA -1: none
     int32_t* err;
     float scale;
-    int heads, groups, Q, W, sinks, min_tiles;
+    int heads, rows_per_seq, row_groups, Q, W, sinks, min_tiles;   // row_groups: rows per query
     bool out_bf16;
 };
 
@@ -182,7 +187,7 @@ struct Walk {
         left -= len;
         t = 0;
         if (left <= 0) return;
-        if (++rq == P.Q * P.groups) {
+        if (++rq == P.rows_per_seq) {
             rq = 0;
             s = seq_info(P, ++b);
         }
@@ -192,10 +197,6 @@ struct Walk {
         return i < s.nc ? kChunk * (i < s.cs ? i : s.wl + i - s.cs) : -1;
     }
 };
-__device__ __forceinline__ bool sees(const Params& P, int t, int p) {
-    return t <= p && (P.W == 0 || t < P.sinks || t > p - P.W);
-}
-
 // ---- numbers --------------------------------------------------------------------------------
 // Eight E2M1 codes (one word) -> eight bytes of the table tab with the codes' signs.
 __device__ __forceinline__ void decode8(uint32_t w, uint2 tab, uint32_t& lo, uint32_t& hi) {
@@ -218,108 +219,211 @@ __device__ __forceinline__ uint32_t f32x2_to_f16x2(float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// ---- the query ---------------------------------------------------------------------------------
-// A fragments of 16 heads' queries: lane (g, c) holds heads g and g + 8, of every 32-dim step the dims 8c..8c+7
-// (f16: two 16-dim MMA steps, the dims in the order that the lane's eight key bytes come in), of every 16-dim
-// RoPE step the dims 4c..4c+3 (bf16), scaled per head by a power of two so that its largest value lies in
-// 2^7..2^8: exact in f16 down to 2^-21 of it.
-struct Query {
-    uint32_t f[kSteps][2][4], rope[4][4];
-    float c2[2];         // logit factor (log2 units) of the two heads
-    __device__ __forceinline__ void load(const Params& P, int b, int rq, int g, int c) {
-        const int j = rq / P.groups, h0 = 16 * (rq % P.groups) + g;
-        const uint16_t* q0 = P.q + (((int64_t)b * P.Q + j) * P.heads + h0) * kDim;
-        uint32_t top[2] = {0, 0};
-#pragma unroll
-        for (int s = 0; s < kSteps; ++s)
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const uint4 v = h0 + 8 * r < P.heads ? __ldg(reinterpret_cast<const uint4*>(q0 + 8 * r * kDim + 32 * s + 8 * c))
-                                                     : make_uint4(0, 0, 0, 0);
-                f[s][0][r] = v.x;
-                f[s][0][2 + r] = v.y;
-                f[s][1][r] = v.z;
-                f[s][1][2 + r] = v.w;
-            }
-#pragma unroll
-        for (int s = 0; s < 4; ++s)
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const uint2 v = h0 + 8 * r < P.heads
-                                    ? __ldg(reinterpret_cast<const uint2*>(q0 + 8 * r * kDim + kNope + 16 * s + 4 * c)) : make_uint2(0, 0);
-                rope[s][r] = v.x;
-                rope[s][2 + r] = v.y;
-            }
-        auto peak = [&](int i, uint32_t x) { top[i & 1] = max(top[i & 1], max(x & 0x7FFFu, (x >> 16) & 0x7FFFu)); };
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-#pragma unroll
-            for (int s = 0; s < kSteps; ++s) {
-                peak(i, f[s][0][i]);
-                peak(i, f[s][1][i]);
-            }
-#pragma unroll
-            for (int s = 0; s < 4; ++s) peak(i, rope[s][i]);
-        }
-        float sq[2];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            top[r] = max(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
-            top[r] = max(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
-            const int sh = top[r] ? max(-100, min(100, 134 - static_cast<int>(top[r] >> 7))) : 0;
-            sq[r] = pow2f(sh);
-            c2[r] = P.scale * 1.4426950408889634f / sq[r];
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-#pragma unroll
-            for (int s = 0; s < kSteps; ++s)
-#pragma unroll
-                for (int u = 0; u < 2; ++u)
-                    f[s][u][i] = f32x2_to_f16x2(bf16_bits_to_f32(f[s][u][i]) * sq[i & 1], bf16_bits_to_f32(f[s][u][i] >> 16) * sq[i & 1]);
-#pragma unroll
-            for (int s = 0; s < 4; ++s)
-                rope[s][i] = f32x2_to_bf16x2_bits(bf16_bits_to_f32(rope[s][i]) * sq[i & 1], bf16_bits_to_f32(rope[s][i] >> 16) * sq[i & 1]);
-        }
-    }
-};
-
 __device__ __forceinline__ void store_out2(const Params& P, int64_t at, float a, float b) {
     if (P.out_bf16) *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(P.out) + at) = f32x2_to_bf16x2_bits(a, b);
     else *reinterpret_cast<float2*>(reinterpret_cast<float*>(P.out) + at) = make_float2(a, b);
 }
 
+// ---- the query ---------------------------------------------------------------------------------
+// A row's A fragments, by all 256 score threads (warp 0..7): each head scaled by a power of two so that its largest
+// value lies in 2^7..2^8 (exact in f16 down to 2^-21 of it; scale_query finds it).  MMA step k < 28 holds of every 32 dims half
+// (k % 2), lane (g, c) the dims 8c + 4 (k % 2) .. + 3 of heads g and g + 8: the order in which a lane's eight key
+// bytes come; steps 28..31 the RoPE dims 16 (k - 28) + 4c .. + 3 in bf16.
+template <bool kFp4, int R>
+__device__ __forceinline__ void scale_query(Smem<kFp4, R>& sm, const Params& P, int b, int rq, int warp, int lane) {
+    const int j = rq / P.row_groups, hr = 16 * R * (rq % P.row_groups);   // the row's first head
+    const uint16_t* q = P.q + (((int64_t)b * P.Q + j) * P.heads + hr) * kDim;
+    // largest value of head 2 warp + lane / 16, by 16 lanes of 32 dims each
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int h = 16 * r + 2 * warp + (lane >> 4);
+        uint32_t top = 0;
+        if (hr + h < P.heads) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint4 v = __ldg(reinterpret_cast<const uint4*>(q + h * kDim) + 4 * (lane & 15) + i);
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) top = max(top, max(w[k] & 0x7FFFu, (w[k] >> 16) & 0x7FFFu));
+            }
+        }
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const int sh = top ? max(-100, min(100, 134 - static_cast<int>(top >> 7))) : 0;
+        if ((lane & 15) == 0) {
+            sm.c2[r][2 * warp + (lane >> 4)] = P.scale * 1.4426950408889634f * pow2f(-sh);
+            sm.sq[r][2 * warp + (lane >> 4)] = pow2f(sh);
+        }
+    }
+}
+template <bool kFp4, int R>
+__device__ __forceinline__ void build_fragments(Smem<kFp4, R>& sm, const Params& P, int b, int rq, int warp, int lane) {
+    const int j = rq / P.row_groups, hr = 16 * R * (rq % P.row_groups), g = lane >> 2, c = lane & 3;
+    const uint16_t* q = P.q + (((int64_t)b * P.Q + j) * P.heads + hr) * kDim;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const float s[2] = {sm.sq[r][g], sm.sq[r][g + 8]};
+#pragma unroll
+        for (int i = 0; i < kQSteps / kScoreWarps; ++i) {
+            const int k = warp * (kQSteps / kScoreWarps) + i;
+            const int d = k < 2 * kSteps ? 32 * (k >> 1) + 8 * c + 4 * (k & 1) : kNope + 16 * (k - 2 * kSteps) + 4 * c;
+            uint32_t a[4];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int h = 16 * r + g + 8 * u;
+                const uint2 v = hr + h < P.heads ? __ldg(reinterpret_cast<const uint2*>(q + h * kDim + d)) : make_uint2(0, 0);
+                const uint32_t w[2] = {v.x, v.y};
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    const float x0 = bf16_bits_to_f32(w[n]) * s[u], x1 = bf16_bits_to_f32(w[n] >> 16) * s[u];
+                    a[u + 2 * n] = k < 2 * kSteps ? f32x2_to_f16x2(x0, x1) : f32x2_to_bf16x2_bits(x0, x1);
+                }
+            }
+            sm.qf[r][k][lane] = make_uint4(a[0], a[1], a[2], a[3]);
+        }
+    }
+}
+
 // ---- score warps ---------------------------------------------------------------------------------
-template <bool kFp4>
-__device__ __forceinline__ void score_role(Smem<kFp4>& sm, const Params& P, Walk wk, int w, int lane, int64_t u1, int64_t n_cta,
+// One MMA of f16 (or, for the RoPE steps, bf16) with an A fragment from shared memory.
+__device__ __forceinline__ void mma_frag(float (&d)[4], const uint4& a, uint32_t b0, uint32_t b1) {
+    const uint32_t f[4] = {a.x, a.y, a.z, a.w};
+    mma_f16(d, f, b0, b1);
+}
+
+// S of this warp's 16 entries, fp4: decodes them (into the value image too).  kFar: some group lies more than 2^26 below
+// its entry's largest, or is NaN.
+template <int R, bool kFar>
+__device__ __forceinline__ void score_fp4(Smem<true, R>& sm, const uint8_t* ch, uint8_t* img, const uint32_t (&at)[4], uint32_t vis,
+                                          int g, int c, int lane, float (&acc)[R][2][2][4]) {
+    int base[2];
+    uint32_t tx[2], ty[2], dx[2], dy[2];
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt) {
+        const bool see = (vis >> (8 * nt + g)) & 1;   // masked: every byte decodes to a signed zero
+        base[nt] = ch[kChunk4Exp + kGroups * kChunk + 8 * nt + g];
+        tx[nt] = see ? kTabX : 0u;
+        ty[nt] = see ? kTabY : 0u;
+        dx[nt] = see ? kTabDx : 0u;
+        dy[nt] = see ? kTabDy : 0u;
+    }
+    // words, exponents and fragments come two steps at a time, the words a round ahead of their use (a load may not pass a
+    // store to the image, as far as the compiler knows)
+    uint32_t wd[2][2][2];
+    int ex[2][2][2];
+    auto fetch = [&](int rd) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt) {
+                const int s = 2 * rd + i;
+                wd[rd & 1][i][nt] = *reinterpret_cast<const uint32_t*>(ch + s * 256 + (8 * nt + g) * 16 + 4 * c);
+                ex[rd & 1][i][nt] = ch[kChunk4Exp + s * kChunk + 8 * nt + g];
+            }
+    };
+    fetch(0);
+#pragma unroll
+    for (int rd = 0; rd < kSteps / 2; ++rd) {
+        uint4 a[R][4];
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) a[r][k] = sm.qf[r][4 * rd + k][lane];
+        if (rd + 1 < kSteps / 2) fetch(rd + 1);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt) {
+                const int s = 2 * rd + i, j = base[nt] - ex[rd & 1][i][nt];
+                uint2 tab = make_uint2(tx[nt] - j * dx[nt], ty[nt] - j * dy[nt]);
+                if (kFar && dx[nt] && (j < 0 || j > kMaxJ)) tab.x = tab.y = j < 0 ? 0x7F7F7F7Fu : 0u;
+                uint32_t b0, b1;
+                decode8(wd[rd & 1][i][nt], tab, b0, b1);
+                *reinterpret_cast<uint2*>(img + (s >> 2) * kBlkBytes + nt * 1024 + at[s & 3]) = make_uint2(b0, b1);
+                const uint32_t f0 = bytes_to_f16x2<true, 0>(b0), f1 = bytes_to_f16x2<true, 1>(b0);
+                const uint32_t f2 = bytes_to_f16x2<true, 0>(b1), f3 = bytes_to_f16x2<true, 1>(b1);
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    mma_frag(acc[r][nt][0], a[r][2 * i], f0, f1);
+                    mma_frag(acc[r][nt][1], a[r][2 * i + 1], f2, f3);
+                }
+            }
+    }
+}
+template <int R>
+__device__ __forceinline__ void score_fp8(Smem<false, R>& sm, const uint8_t* img, const uint32_t (&at)[4], int lane, float (&acc)[R][2][2][4]) {
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+        uint4 a[R][2];
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) a[r][k] = sm.qf[r][2 * s + k][lane];
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+            const uint2 b = *reinterpret_cast<const uint2*>(img + (s >> 2) * kBlkBytes + nt * 1024 + at[s & 3]);
+            const uint32_t f0 = bytes_to_f16x2<false, 0>(b.x), f1 = bytes_to_f16x2<false, 1>(b.x);
+            const uint32_t f2 = bytes_to_f16x2<false, 0>(b.y), f3 = bytes_to_f16x2<false, 1>(b.y);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                mma_frag(acc[r][nt][0], a[r][0], f0, f1);
+                mma_frag(acc[r][nt][1], a[r][1], f2, f3);
+            }
+        }
+    }
+}
+
+template <bool kFp4, int R>
+__device__ __forceinline__ void score_role(Smem<kFp4, R>& sm, const Params& P, Walk wk, int warp, int lane, int64_t u1, int64_t n_cta,
                                            int64_t total) {
-    constexpr int kStages = Smem<kFp4>::kStages;
+    constexpr int kS = Smem<kFp4, R>::kStages;
     volatile int32_t* fail = &sm.fail;
-    const int g = lane >> 2, c = lane & 3;
+    const int gr = warp >> 2, w = warp & 3, g = lane >> 2, c = lane & 3;   // group gr takes the tiles T % 2 == gr
     // place of this lane's eight bytes of step s, entry n = 8 nt + g of chunk w: block s / 4, row 16 w + n
     uint32_t at[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) at[q] = (16 * w + g) * 128 + ((((c >> 1) ^ g) ^ (2 * q)) << 4) + 8 * (c & 1);
-    Query qy;
     int T = 0, seg = 0;
     for (; wk.left > 0; wk.next(P), ++seg) {
-        qy.load(P, wk.b, wk.rq, g, c);
-        const int p = wk.s.n - P.Q + wk.rq / P.groups;   // the query's position
-        float nm[2] = {kUnset, kUnset}, l[2] = {0.f, 0.f}, gs = 0.f;   // gs = 0: g not set yet
-        for (int t = 0; t < wk.len; ++t, ++T) {
-            const int st = T % kStages, buf = T & 1;
-            bool ok = wait(&sm.full[st], (T / kStages) & 1, fail);
+        named_barrier(kBarScore, 32 * kScoreWarps);   // the last row's fragments and marks are done with
+        scale_query<kFp4, R>(sm, P, wk.b, wk.rq, warp, lane);
+        if (warp == 0) {
+            if (lane < kHeads)
+#pragma unroll
+                for (int r = 0; r < R; ++r) sm.nm[r][lane] = kUnset;
+            if (lane == 0) sm.gs = 0.f;   // not set yet
+        }
+        named_barrier(kBarScore, 32 * kScoreWarps);
+        build_fragments<kFp4, R>(sm, P, wk.b, wk.rq, warp, lane);
+        named_barrier(kBarScore, 32 * kScoreWarps);
+        const int p = wk.s.n - P.Q + wk.rq / P.row_groups;   // the query's position; it sees t <= p, t > lo or t < sinks
+        const int lo = P.W > 0 ? max(p, 0) - P.W : -1;
+        float nm[R][2], l[R][2], c2[R][2];   // heads g, g + 8; l is relative to nm
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                nm[r][k] = kUnset;
+                l[r][k] = 0.f;
+                c2[r][k] = sm.c2[r][g + 8 * k];
+            }
+        const int T0 = T, T1 = T + wk.len;
+        for (T += (T ^ gr) & 1; T < T1; T += 2) {
+            const int st = T % kS, buf = T & 1;
+            bool ok = wait(&sm.full[st], (T / kS) & 1, fail);
             if (T >= 2) ok = ok && wait(&sm.pempty[buf], ((T >> 1) - 1) & 1, fail);
             ok = __all_sync(0xffffffffu, ok);
-            const int tok0 = ok ? sm.chunk_tok[st][w] : -1;
-            auto sees_entry = [&](int en) { return tok0 >= 0 && sees(P, tok0 + en, p); };
-            float acc[2][2][4], racc[2][4];   // [entries 8 nt ..][half of a step: independent chains], RoPE part
+            const int tok0 = ok ? sm.chunk_tok[st][w] : -1, tk = tok0 + (lane & 15);
+            const uint32_t vis = __ballot_sync(0xffffffffu, tok0 >= 0 && tk <= p && (tk > lo || tk < P.sinks)) & 0xFFFFu;
+            float acc[R][2][2][4], racc[R][2][4];   // [entries 8 nt ..][half of a step: independent chains]; RoPE part
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt)
+            for (int r = 0; r < R; ++r)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) acc[nt][0][i] = acc[nt][1][i] = racc[nt][i] = 0.f;
+                for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[r][nt][0][i] = acc[r][nt][1][i] = racc[r][nt][i] = 0.f;
             uint8_t* img = kFp4 ? sm.img[kFp4 ? buf : 0] : sm.stage[st];
-            float fe[2][2];   // of the entries 8 nt + 2 c + i: the columns of this lane's scores
+            float fe[2][2];   // of the entries 8 nt + 2 c + i: the columns of this lane's scores; 0: masked
             if constexpr (kFp4) {
                 const uint8_t* ch = sm.stage[st] + w * kChunk4Bytes;
                 // RoPE rows into the image, eight lanes a row
@@ -327,138 +431,106 @@ __device__ __forceinline__ void score_role(Smem<kFp4>& sm, const Params& P, Walk
                 for (int i = 0; i < 4; ++i) {
                     const int en = 4 * i + (lane >> 3), k = lane & 7;
                     uint4 v = *reinterpret_cast<const uint4*>(ch + kChunk4Rope + en * 2 * kRope + 16 * k);
-                    if (!sees_entry(en)) v = make_uint4(0, 0, 0, 0);
+                    if (!((vis >> en) & 1)) v = make_uint4(0, 0, 0, 0);
                     *reinterpret_cast<uint4*>(img + 4 * kBlkBytes + sw128(16 * w + en, 16 * k)) = v;
                 }
-                int base[2];
-                uint32_t tx[2], ty[2], dx[2], dy[2];
+                // groups whose scale lies far below the entry's largest (zero there), or NaN groups (byte 255).  Lane (g, c) looks
+                // at the groups c, c + 4, .. of entries g and 8 + g
+                uint32_t most = 0;
 #pragma unroll
                 for (int nt = 0; nt < 2; ++nt) {
-                    const bool vis = sees_entry(8 * nt + g);   // masked: every byte decodes to a signed zero
-                    base[nt] = ch[kChunk4Exp + kGroups * kChunk + 8 * nt + g];
-                    tx[nt] = vis ? kTabX : 0u;
-                    ty[nt] = vis ? kTabY : 0u;
-                    dx[nt] = vis ? kTabDx : 0u;
-                    dy[nt] = vis ? kTabDy : 0u;
+                    const int base = ch[kChunk4Exp + kGroups * kChunk + 8 * nt + g];
+#pragma unroll
+                    for (int s = 0; s < 4; ++s)
+                        if (4 * s + c < kSteps && (vis >> (8 * nt + g)) & 1)
+                            most = max(most, static_cast<uint32_t>(base - ch[kChunk4Exp + (4 * s + c) * kChunk + 8 * nt + g]));
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const uint32_t eb = ch[kChunk4Exp + kGroups * kChunk + 8 * nt + 2 * c + i];
-                        fe[nt][i] = __uint_as_float(eb << 23) * 0x1p-13f;
+                        fe[nt][i] = (vis >> (8 * nt + 2 * c + i)) & 1 ? __uint_as_float(eb << 23) * 0x1p-13f : 0.f;
                     }
                 }
-                // j above kMaxJ (a group of 2^-26 of the entry's largest: zero) or below 0 (a NaN group) in some entry.
-                // Lane (g, c) looks at the groups c, c + 4, ..
-                uint32_t most = 0;
-#pragma unroll
-                for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-                    for (int s = 0; s < 4; ++s)
-                        if (dx[nt] && 4 * s + c < kSteps)
-                            most = max(most, static_cast<uint32_t>(base[nt] - ch[kChunk4Exp + (4 * s + c) * kChunk + 8 * nt + g]));
-                const bool far = __any_sync(0xffffffffu, most > kMaxJ);
-                // words and exponents come in blocks of four steps, a block ahead of their use (a load may not pass a
-                // store to the image, as far as the compiler knows)
-                uint32_t wd[2][4][2];
-                int ex[2][4][2];
-                auto fetch = [&](int blk) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int nt = 0; nt < 2; ++nt) {
-                            const int s = 4 * blk + i;
-                            if (s >= kSteps) continue;
-                            wd[blk & 1][i][nt] = *reinterpret_cast<const uint32_t*>(ch + s * 256 + (8 * nt + g) * 16 + 4 * c);
-                            ex[blk & 1][i][nt] = ch[kChunk4Exp + s * kChunk + 8 * nt + g];
-                        }
-                };
-                fetch(0);
-#pragma unroll
-                for (int blk = 0; blk < 4; ++blk) {
-                    if (blk < 3) fetch(blk + 1);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int nt = 0; nt < 2; ++nt) {
-                            const int s = 4 * blk + i;
-                            if (s >= kSteps) continue;
-                            const int j = base[nt] - ex[blk & 1][i][nt];
-                            uint2 tab = make_uint2(tx[nt] - j * dx[nt], ty[nt] - j * dy[nt]);
-                            if (far && dx[nt] && (j < 0 || j > kMaxJ)) tab.x = tab.y = j < 0 ? 0x7F7F7F7Fu : 0u;
-                            uint32_t b0, b1;
-                            decode8(wd[blk & 1][i][nt], tab, b0, b1);
-                            *reinterpret_cast<uint2*>(img + blk * kBlkBytes + nt * 1024 + at[i]) = make_uint2(b0, b1);
-                            mma_f16(acc[nt][0], qy.f[s][0], bytes_to_f16x2<true, 0>(b0), bytes_to_f16x2<true, 1>(b0));
-                            mma_f16(acc[nt][1], qy.f[s][1], bytes_to_f16x2<true, 0>(b1), bytes_to_f16x2<true, 1>(b1));
-                        }
-                }
+                if (__any_sync(0xffffffffu, most > static_cast<uint32_t>(kMaxJ))) score_fp4<R, true>(sm, ch, img, at, vis, g, c, lane, acc);
+                else score_fp4<R, false>(sm, ch, img, at, vis, g, c, lane, acc);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.empty[st]);
             } else {
-                fe[0][0] = fe[0][1] = fe[1][0] = fe[1][1] = 1.f;
-                // masked rows are zeroed for the value warps
-                if (!__all_sync(0xffffffffu, sees_entry(lane & 15))) {
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) fe[nt][i] = (vis >> (8 * nt + 2 * c + i)) & 1 ? 1.f : 0.f;
+                if (vis != 0xFFFFu) {   // masked rows are zeroed for the value warps
                     for (int en = 0; en < 16; ++en)
-                        if (!sees_entry(en))
+                        if (!((vis >> en) & 1))
                             for (int k = lane; k < 40; k += 32)
                                 *reinterpret_cast<uint4*>(img + (k >> 3) * kBlkBytes + sw128(16 * w + en, 16 * (k & 7))) = make_uint4(0, 0, 0, 0);
                     fence_proxy_async_smem();   // the ring's next copy writes there too
                     __syncwarp();
                 }
-#pragma unroll
-                for (int s = 0; s < kSteps; ++s)
-#pragma unroll
-                    for (int nt = 0; nt < 2; ++nt) {
-                        const uint2 b = *reinterpret_cast<const uint2*>(img + (s >> 2) * kBlkBytes + nt * 1024 + at[s & 3]);
-                        mma_f16(acc[nt][0], qy.f[s][0], bytes_to_f16x2<false, 0>(b.x), bytes_to_f16x2<false, 1>(b.x));
-                        mma_f16(acc[nt][1], qy.f[s][1], bytes_to_f16x2<false, 0>(b.y), bytes_to_f16x2<false, 1>(b.y));
-                    }
+                score_fp8<R>(sm, img, at, lane, acc);
             }
 #pragma unroll
-            for (int s = 0; s < 4; ++s)
+            for (int s = 0; s < 4; ++s) {
+                uint4 a[R];
+#pragma unroll
+                for (int r = 0; r < R; ++r) a[r] = sm.qf[r][2 * kSteps + s][lane];
 #pragma unroll
                 for (int nt = 0; nt < 2; ++nt) {
                     const uint2 b = *reinterpret_cast<const uint2*>(img + 4 * kBlkBytes + nt * 1024 + at[s]);
-                    mma_bf16(racc[nt], qy.rope[s][0], qy.rope[s][1], qy.rope[s][2], qy.rope[s][3], b.x, b.y);
+#pragma unroll
+                    for (int r = 0; r < R; ++r) mma_bf16(racc[r][nt], a[r].x, a[r].y, a[r].z, a[r].w, b.x, b.y);
                 }
-            // logits x[nt][2 r + i]: entry 8 nt + 2 c + i, head g + 8 r (log2 units), -inf where masked
-            float x[2][4];
-            bool see[2][2];
+            }
+            // logits x[r][nt][2 k + i]: entry 8 nt + 2 c + i, head g + 8 k (log2 units), -inf where masked
+            float (&x)[R][2][4] = racc;
+            float top[R][2], fmost = fmaxf(fmaxf(fe[0][0], fe[0][1]), fmaxf(fe[1][0], fe[1][1]));
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt)
+            for (int r = 0; r < R; ++r)
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    see[nt][i] = sees_entry(8 * nt + 2 * c + i);
+                for (int k = 0; k < 2; ++k) {
+                    top[r][k] = -INFINITY;
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        const int k = 2 * r + i;
-                        const float v = kFp4 ? fmaf(acc[nt][0][k] + acc[nt][1][k], fe[nt][i], racc[nt][k])
-                                             : (acc[nt][0][k] + acc[nt][1][k]) + racc[nt][k];
-                        x[nt][k] = see[nt][i] ? v * qy.c2[r] : -INFINITY;
-                    }
-                    if (!see[nt][i]) fe[nt][i] = 0.f;
+                    for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int n = 2 * k + i;
+                            const float sum = acc[r][nt][0][n] + acc[r][nt][1][n];
+                            const float v = kFp4 ? fmaf(sum, fe[nt][i], racc[r][nt][n]) : sum + racc[r][nt][n];
+                            x[r][nt][n] = fe[nt][i] > 0.f ? v * c2[r][k] : -INFINITY;
+                            top[r][k] = fmaxf(top[r][k], x[r][nt][n]);
+                        }
                 }
-            float top[2], fmost = fmaxf(fmaxf(fe[0][0], fe[0][1]), fmaxf(fe[1][0], fe[1][1]));
+            // the marks, as the tile before left them
+            if (T > 0) (void)wait(&sm.marked[(T - 1) & 1], ((T - 1) >> 1) & 1, fail);
+            float gs = sm.gs, mk[R][2];
+            bool over = kFp4 && fmost * gs > kFeMost;
 #pragma unroll
-            for (int r = 0; r < 2; ++r) top[r] = fmaxf(fmaxf(x[0][2 * r], x[0][2 * r + 1]), fmaxf(x[1][2 * r], x[1][2 * r + 1]));
-            const bool over = top[0] + nm[0] > kOver<kFp4> || top[1] + nm[1] > kOver<kFp4> || (kFp4 && fmost * gs > kFeMost);
-            int resc = t == 0 ? 2 : 0;
-            if (named_barrier_or(kBarScore, 32 * kScoreWarps, over)) {
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    mk[r][k] = sm.nm[r][g + 8 * k];
+                    over |= top[r][k] + mk[r][k] > kOver<kFp4>;
+                }
+            int resc = T == T0 ? 2 : 0;
+            if (named_barrier_or(kBarGroup + gr, 32 * kGroupWarps, over)) {
                 // some weight is too large, or the first tile: the tile's maxima; a head that lies more than 2 above its
                 // mark gets a new one, and the value warps the factors of what they hold
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
-                    top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
-                    if (c == 0) sm.tmax[w][g + 8 * r] = top[r];
-                }
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        top[r][k] = fmaxf(top[r][k], __shfl_xor_sync(0xffffffffu, top[r][k], 1));
+                        top[r][k] = fmaxf(top[r][k], __shfl_xor_sync(0xffffffffu, top[r][k], 2));
+                        if (c == 0) sm.tmax[gr][w][r][g + 8 * k] = top[r][k];
+                    }
                 if constexpr (kFp4) {
                     const uint32_t fm = __reduce_max_sync(0xffffffffu, __float_as_uint(fmost));
-                    if (lane == 0) sm.femax[w] = __uint_as_float(fm);
+                    if (lane == 0) sm.femax[gr][w] = __uint_as_float(fm);
                 }
-                named_barrier(kBarScore, 32 * kScoreWarps);
+                named_barrier(kBarGroup + gr, 32 * kGroupWarps);
                 float fg = 1.f;
                 if constexpr (kFp4) {
-                    const float fm = fmaxf(fmaxf(sm.femax[0], sm.femax[1]), fmaxf(sm.femax[2], sm.femax[3]));
+                    const float fm = fmaxf(fmaxf(sm.femax[gr][0], sm.femax[gr][1]), fmaxf(sm.femax[gr][2], sm.femax[gr][3]));
                     if (fm > 0.f && (gs == 0.f || fm * gs > kFeMost)) {
                         const float gn = kFeSet / fmaxf(fm, 0x1p-110f);
                         if (gs != 0.f) fg = gn / gs;
@@ -466,57 +538,78 @@ __device__ __forceinline__ void score_role(Smem<kFp4>& sm, const Params& P, Walk
                     }
                 }
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    float tm = sm.tmax[0][g + 8 * r];
+                for (int r = 0; r < R; ++r)
 #pragma unroll
-                    for (int k = 1; k < kScoreWarps; ++k) tm = fmaxf(tm, sm.tmax[k][g + 8 * r]);
-                    const bool first = nm[r] == kUnset;
-                    const bool set = first ? tm > -INFINITY : tm + nm[r] > kLift<kFp4> + 2.f;
-                    const float to = set ? kLift<kFp4> - tm : nm[r];
-                    const float f = set && !first ? exp2_ftz(to - nm[r]) : 1.f;
-                    l[r] *= f;
-                    nm[r] = to;
-                    if (w == 0 && c == 0) {
-                        sm.fn[buf][g + 8 * r] = f * fg;
-                        sm.fr[buf][g + 8 * r] = f;
+                    for (int k = 0; k < 2; ++k) {
+                        float tm = sm.tmax[gr][0][r][g + 8 * k];
+#pragma unroll
+                        for (int i = 1; i < kGroupWarps; ++i) tm = fmaxf(tm, sm.tmax[gr][i][r][g + 8 * k]);
+                        const bool first = mk[r][k] == kUnset;
+                        const bool set = first ? tm > -INFINITY : tm + mk[r][k] > kLift<kFp4> + 2.f;
+                        const float to = set ? kLift<kFp4> - tm : mk[r][k];
+                        const float f = set && !first ? exp2_ftz(to - mk[r][k]) : 1.f;
+                        mk[r][k] = to;
+                        if (w == 0 && c == 0) {
+                            sm.fn[buf][r][g + 8 * k] = f * fg;
+                            sm.fr[buf][r][g + 8 * k] = f;
+                            sm.nm[r][g + 8 * k] = to;
+                        }
                     }
-                }
-                if (t > 0) resc = 1;
+                if (w == 0 && lane == 0) sm.gs = gs;
+                if (T > T0) resc = 1;
+            }
+            if (w == 0) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.marked[buf]);
             }
             // P: p = 2^(x + nm), as A fragments: of the chunk's 16 entries a lane holds 8 nt + 2 c + i, the MMA's k slots
             // 2c + i (nt = 0) and 2c + 8 + i
-            uint32_t pb[2][2], ph[2][2];   // [r][nt]
 #pragma unroll
-            for (int r = 0; r < 2; ++r)
+            for (int r = 0; r < R; ++r) {
+                uint32_t pb[2][2], ph[2][2];   // [head][nt]
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt) {
-                    const float p0 = exp2_ftz(x[nt][2 * r] + nm[r]), p1 = exp2_ftz(x[nt][2 * r + 1] + nm[r]);
-                    l[r] += p0 + p1;
-                    pb[r][nt] = f32x2_to_bf16x2_bits(p0, p1);
-                    ph[r][nt] = kFp4 ? f32x2_to_f16x2(p0 * (fe[nt][0] * gs), p1 * (fe[nt][1] * gs)) : f32x2_to_f16x2(p0, p1);
+                for (int k = 0; k < 2; ++k) {
+                    if (mk[r][k] != nm[r][k]) {   // the mark moved, in this tile or in the other group's
+                        l[r][k] *= exp2_ftz(mk[r][k] - nm[r][k]);
+                        nm[r][k] = mk[r][k];
+                    }
+#pragma unroll
+                    for (int nt = 0; nt < 2; ++nt) {
+                        const float p0 = exp2_ftz(x[r][nt][2 * k] + nm[r][k]), p1 = exp2_ftz(x[r][nt][2 * k + 1] + nm[r][k]);
+                        l[r][k] += p0 + p1;
+                        pb[k][nt] = f32x2_to_bf16x2_bits(p0, p1);
+                        ph[k][nt] = kFp4 ? f32x2_to_f16x2(p0 * (fe[nt][0] * gs), p1 * (fe[nt][1] * gs)) : f32x2_to_f16x2(p0, p1);
+                    }
                 }
-            sm.p16[buf][w][lane] = make_uint4(ph[0][0], ph[1][0], ph[0][1], ph[1][1]);
-            sm.pbf[buf][w][lane] = make_uint4(pb[0][0], pb[1][0], pb[0][1], pb[1][1]);
+                sm.p16[buf][r][w][lane] = make_uint4(ph[0][0], ph[1][0], ph[0][1], ph[1][1]);
+                sm.pbf[buf][r][w][lane] = make_uint4(pb[0][0], pb[1][0], pb[0][1], pb[1][1]);
+            }
             if (w == 0 && lane == 0) sm.resc[buf] = resc;
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.pfull[buf]);
         }
-        // ---- the segment's sums --------------------------------------------------------------------
+        T = T1;
+        // ---- the segment's sums, relative to the last marks --------------------------------------------
         const int sb = seg & 1;
+        (void)wait(&sm.marked[(T1 - 1) & 1], ((T1 - 1) >> 1) & 1, fail);
         if (seg >= 2) (void)wait(&sm.segempty[sb], ((seg >> 1) - 1) & 1, fail);
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-            if (c == 0) {
-                sm.lsum[sb][w][g + 8 * r] = l[r];
-                if (w == 0) sm.mseg[sb][g + 8 * r] = -nm[r];
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const float mk = sm.nm[r][g + 8 * k];
+                float v = mk != nm[r][k] ? l[r][k] * exp2_ftz(mk - nm[r][k]) : l[r][k];
+                v += __shfl_xor_sync(0xffffffffu, v, 1);
+                v += __shfl_xor_sync(0xffffffffu, v, 2);
+                if (c == 0) {
+                    sm.lsum[sb][warp][r][g + 8 * k] = v;
+                    if (warp == 0) sm.mseg[sb][r][g + 8 * k] = -mk;
+                }
             }
-        }
-        if (w == 0 && lane == 0) {
-            sm.ginv[sb] = gs != 0.f ? 1.f / gs : 1.f;
+        if (warp == 0 && lane == 0) {
+            sm.ginv[sb] = sm.gs != 0.f ? 1.f / sm.gs : 1.f;
             if (wk.t == 0 && wk.len < wk.s.tiles) {   // a cut row begins here: which CTA holds its end
-                const int64_t row = (int64_t)wk.b * P.Q * P.groups + wk.rq;
+                const int64_t row = (int64_t)wk.b * P.rows_per_seq + wk.rq;
                 const int64_t end = u1 - wk.left + wk.s.tiles;    // unit behind the row
                 int64_t e = (end - 1) * n_cta / total;
                 while (total * (e + 1) / n_cta <= end - 1) ++e;
@@ -530,9 +623,9 @@ __device__ __forceinline__ void score_role(Smem<kFp4>& sm, const Params& P, Walk
 }
 
 // ---- value warps ---------------------------------------------------------------------------------
-template <bool kFp4>
-__device__ __forceinline__ void value_role(Smem<kFp4>& sm, const Params& P, Walk wk, int w, int lane) {
-    constexpr int kStages = Smem<kFp4>::kStages;
+template <bool kFp4, int R>
+__device__ __forceinline__ void value_role(Smem<kFp4, R>& sm, const Params& P, Walk wk, int w, int lane) {
+    constexpr int kS = Smem<kFp4, R>::kStages;
     volatile int32_t* fail = &sm.fail;
     const int g = lane >> 2, c = lane & 3;
     const bool rope = w == kValueWarps - 1;
@@ -548,29 +641,34 @@ __device__ __forceinline__ void value_role(Smem<kFp4>& sm, const Params& P, Walk
         col = lane >> 4;
     }
     const uint32_t off = (rope ? 4 : w >> 1) * kBlkBytes + (row >> 3) * 1024 + (row & 7) * 128;
-    float o[8][4];
+    float o[R][8][4];
     int T = 0, seg = 0;
     for (; wk.left > 0; wk.next(P), ++seg) {
         for (int t = 0; t < wk.len; ++t, ++T) {
-            const int buf = T & 1, st = T % kStages;
+            const int buf = T & 1, st = T % kS;
             bool ok = wait(&sm.pfull[buf], (T >> 1) & 1, fail);
-            if (!kFp4) ok = ok && wait(&sm.full[st], (T / kStages) & 1, fail);   // complete: makes the copy visible here
+            if (!kFp4) ok = ok && wait(&sm.full[st], (T / kS) & 1, fail);   // complete: makes the copy visible here
             ok = __all_sync(0xffffffffu, ok);
             const int resc = sm.resc[buf];
             if (resc == 2) {
 #pragma unroll
-                for (int q = 0; q < 8; ++q)
+                for (int r = 0; r < R; ++r)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) o[q][i] = 0.f;
+                    for (int q = 0; q < 8; ++q)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) o[r][q][i] = 0.f;
             } else if (resc == 1) {
-                const float* f = rope ? sm.fr[buf] : sm.fn[buf];
-                const float f0 = f[g], f1 = f[g + 8];
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    o[q][0] *= f0;
-                    o[q][1] *= f0;
-                    o[q][2] *= f1;
-                    o[q][3] *= f1;
+                for (int r = 0; r < R; ++r) {
+                    const float* f = rope ? sm.fr[buf][r] : sm.fn[buf][r];
+                    const float f0 = f[g], f1 = f[g + 8];
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        o[r][q][0] *= f0;
+                        o[r][q][1] *= f0;
+                        o[r][q][2] *= f1;
+                        o[r][q][3] *= f1;
+                    }
                 }
             }
             if (ok) {
@@ -578,32 +676,40 @@ __device__ __forceinline__ void value_role(Smem<kFp4>& sm, const Params& P, Walk
                 if (!rope) {
 #pragma unroll
                     for (int kb = 0; kb < kTile / 32; ++kb) {
-                        const uint4 p0 = sm.p16[buf][2 * kb][lane], p1 = sm.p16[buf][2 * kb + 1][lane];
-                        const uint32_t a0[4] = {p0.x, p0.y, p0.z, p0.w}, a1[4] = {p1.x, p1.y, p1.z, p1.w};
-                        uint32_t v[4][4];
+                        uint4 a[R][2];
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) ldmatrix_b8_trans_x2(v[q], base + kb * 4096 + (((col + q) ^ (row & 7)) << 4));
+                        for (int r = 0; r < R; ++r)
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            mma_f16(o[2 * q], a0, bytes_to_f16x2<kFp4, 0>(v[q][0]), bytes_to_f16x2<kFp4, 1>(v[q][0]));
-                            mma_f16(o[2 * q + 1], a0, bytes_to_f16x2<kFp4, 0>(v[q][1]), bytes_to_f16x2<kFp4, 1>(v[q][1]));
-                        }
+                            for (int u = 0; u < 2; ++u) a[r][u] = sm.p16[buf][r][2 * kb + u][lane];
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
-                            mma_f16(o[2 * q], a1, bytes_to_f16x2<kFp4, 0>(v[q][2]), bytes_to_f16x2<kFp4, 1>(v[q][2]));
-                            mma_f16(o[2 * q + 1], a1, bytes_to_f16x2<kFp4, 0>(v[q][3]), bytes_to_f16x2<kFp4, 1>(v[q][3]));
+                            uint32_t v[4];   // dims 16 q + lane / 4 (+ 8: odd), chunk 2 kb (+ 1: v[2], v[3])
+                            ldmatrix_b8_trans_x2(v, base + kb * 4096 + (((col + q) ^ (row & 7)) << 4));
+#pragma unroll
+                            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                                for (int n = 0; n < 2; ++n) {
+                                    const uint32_t b0 = bytes_to_f16x2<kFp4, 0>(v[2 * u + n]), b1 = bytes_to_f16x2<kFp4, 1>(v[2 * u + n]);
+#pragma unroll
+                                    for (int r = 0; r < R; ++r) mma_frag(o[r][2 * q + n], a[r][u], b0, b1);
+                                }
                         }
                     }
                 } else {
 #pragma unroll
                     for (int k = 0; k < kTileChunks; ++k) {
-                        const uint4 a = sm.pbf[buf][k][lane];
+                        uint4 a[R];
+#pragma unroll
+                        for (int r = 0; r < R; ++r) a[r] = sm.pbf[buf][r][k][lane];
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             uint32_t v[4];
                             ldmatrix_b16_trans_x4(v, base + k * 2048 + (((col + 2 * q) ^ (row & 7)) << 4));
-                            mma_bf16(o[2 * q], a.x, a.y, a.z, a.w, v[0], v[1]);
-                            mma_bf16(o[2 * q + 1], a.x, a.y, a.z, a.w, v[2], v[3]);
+#pragma unroll
+                            for (int r = 0; r < R; ++r) {
+                                mma_bf16(o[r][2 * q], a[r].x, a[r].y, a[r].z, a[r].w, v[0], v[1]);
+                                mma_bf16(o[r][2 * q + 1], a[r].x, a[r].y, a[r].z, a[r].w, v[2], v[3]);
+                            }
                         }
                     }
                 }
@@ -617,44 +723,44 @@ __device__ __forceinline__ void value_role(Smem<kFp4>& sm, const Params& P, Walk
         // ---- the segment's result ------------------------------------------------------------------
         const int sb = seg & 1;
         const bool ok = __all_sync(0xffffffffu, wait(&sm.segfull[sb], (seg >> 1) & 1, fail));
-        float L[2], M[2];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int h = g + 8 * r;
-            L[r] = (sm.lsum[sb][0][h] + sm.lsum[sb][1][h]) + (sm.lsum[sb][2][h] + sm.lsum[sb][3][h]);
-            M[r] = sm.mseg[sb][h];
-        }
-        const float gi = rope ? 1.f : sm.ginv[sb];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.segempty[sb]);
-        if (!ok) continue;
         const bool whole = wk.t == 0 && wk.len == wk.s.tiles;
-        const int j = wk.rq / P.groups, h0 = 16 * (wk.rq % P.groups) + g;
+        const int j = wk.rq / P.row_groups, h0 = 16 * R * (wk.rq % P.row_groups) + g;
         const int64_t head = ((int64_t)wk.b * P.Q + j) * P.heads + h0;
         const int64_t slot = 2 * (int64_t)blockIdx.x + (wk.t == 0 ? 1 : 0);
+        const float gi = rope ? 1.f : sm.ginv[sb];
+        if (ok) {
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const float f = whole ? (L[r] == 0.f ? 0.f : gi / L[r]) : gi;
+            for (int r = 0; r < R; ++r)
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                const int d = 64 * w + 8 * q + 2 * c;
-                const float v0 = o[q][2 * r] * f, v1 = o[q][2 * r + 1] * f;
-                if (!whole) *reinterpret_cast<float2*>(P.opart + (slot * kHeads + g + 8 * r) * kDim + d) = make_float2(v0, v1);
-                else if (h0 + 8 * r < P.heads) store_out2(P, (head + 8 * r) * kDim + d, v0, v1);
-            }
-            if (w == 0 && c == 0) {
-                if (!whole) P.mlpart[slot * kHeads + g + 8 * r] = make_float2(M[r], L[r]);
-                else if (P.lse && h0 + 8 * r < P.heads)
-                    P.lse[head + 8 * r] = L[r] == 0.f ? -INFINITY : (M[r] + log2f(L[r])) * 0.69314718055994531f;
-            }
+                for (int k = 0; k < 2; ++k) {
+                    const int h = 16 * r + 8 * k;   // from this lane's first head
+                    float L = 0.f;
+#pragma unroll
+                    for (int i = 0; i < kScoreWarps; ++i) L += sm.lsum[sb][i][r][g + 8 * k];
+                    const float M = sm.mseg[sb][r][g + 8 * k], f = whole ? (L == 0.f ? 0.f : gi / L) : gi;
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        const int d = 64 * w + 8 * q + 2 * c;
+                        const float v0 = o[r][q][2 * k] * f, v1 = o[r][q][2 * k + 1] * f;
+                        if (!whole) *reinterpret_cast<float2*>(P.opart + (slot * R * kHeads + g + h) * kDim + d) = make_float2(v0, v1);
+                        else if (h0 + h < P.heads) store_out2(P, (head + h) * kDim + d, v0, v1);
+                    }
+                    if (w == 0 && c == 0) {
+                        if (!whole) P.mlpart[slot * R * kHeads + g + h] = make_float2(M, L);
+                        else if (P.lse && h0 + h < P.heads)
+                            P.lse[head + h] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+                    }
+                }
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.segempty[sb]);
     }
 }
 
 // ---- copy warp -------------------------------------------------------------------------------------
-template <bool kFp4>
-__device__ __forceinline__ void copy_role(Smem<kFp4>& sm, const Params& P, Walk wk, int lane, const CUtensorMap* pages_map) {
-    constexpr int kStages = Smem<kFp4>::kStages;
+template <bool kFp4, int R>
+__device__ __forceinline__ void copy_role(Smem<kFp4, R>& sm, const Params& P, Walk wk, int lane, const CUtensorMap* pages_map) {
+    constexpr int kS = Smem<kFp4, R>::kStages;
     volatile int32_t* fail = &sm.fail;
     int T = 0;
     // lane i < 4: chunk i of the tile; its first token and page, loaded one tile ahead
@@ -668,9 +774,9 @@ __device__ __forceinline__ void copy_role(Smem<kFp4>& sm, const Params& P, Walk 
         look(wk, 0, tok, pg);
         for (int t = 0; t < wk.len; ++t, ++T) {
             if (t + 1 < wk.len) look(wk, t + 1, tok1, pg1);
-            const int st = T % kStages;
+            const int st = T % kS;
             bool ok = !*fail;
-            if (T >= kStages) ok = ok && wait(&sm.empty[st], (T / kStages - 1) & 1, fail);
+            if (T >= kS) ok = ok && wait(&sm.empty[st], (T / kS - 1) & 1, fail);
             if (!__all_sync(0xffffffffu, ok)) return;
             if (tok >= 0 && (pg < 0 || pg >= P.c.n_pages)) {
                 dev_error(P.err, CSLD_DEVERR_PAGE);
@@ -702,23 +808,25 @@ __device__ __forceinline__ void copy_role(Smem<kFp4>& sm, const Params& P, Walk 
 
 }  // namespace
 
-template <bool kFp4>
+template <bool kFp4, int R>
 __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __grid_constant__ CUtensorMap pages_map,
                                                                       const __grid_constant__ Params P) {
-    using S = Smem<kFp4>;
+    using S = Smem<kFp4, R>;
+    constexpr int kS = Smem<kFp4, R>::kStages;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     S& sm = *reinterpret_cast<S*>(smem_raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
     // ---- setup --------------------------------------------------------------------------------
     if (tid == 0) {
-        for (int s = 0; s < S::kStages; ++s) {
+        for (int s = 0; s < kS; ++s) {
             mbar_init(&sm.full[s], 1);
-            mbar_init(&sm.empty[s], kFp4 ? kScoreWarps : kValueWarps);
+            mbar_init(&sm.empty[s], kFp4 ? kGroupWarps : kValueWarps);
         }
         for (int s = 0; s < 2; ++s) {
-            mbar_init(&sm.pfull[s], kScoreWarps);
+            mbar_init(&sm.pfull[s], kGroupWarps);
             mbar_init(&sm.pempty[s], kValueWarps);
+            mbar_init(&sm.marked[s], 1);
             mbar_init(&sm.segfull[s], kScoreWarps);
             mbar_init(&sm.segempty[s], kValueWarps);
         }
@@ -731,7 +839,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
     pdl_trigger();
 
     // ---- this CTA's share of all rows' tiles ------------------------------------------------------
-    const int rows_per_seq = P.Q * P.groups;
+    const int rows_per_seq = P.rows_per_seq;
     int64_t mine = 0;
     for (int b = tid; b < P.c.batch; b += kThreads) {
         const int32_t n = P.c.seq_len[b];
@@ -789,20 +897,20 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
         wk.begin(P, sm.b0, u0 - sm.prefix, n_tiles);
         if (warp < kScoreWarps) {
             regs_inc<kRegsScore>();
-            score_role<kFp4>(sm, P, wk, warp, lane, u1, n_cta, total);
+            score_role<kFp4, R>(sm, P, wk, warp, lane, u1, n_cta, total);
         } else if (warp < kValueWarp + kValueWarps) {
-            regs_dec<kRegsValue>();
-            value_role<kFp4>(sm, P, wk, warp - kValueWarp, lane);
+            regs_inc<kRegsValue>();
+            value_role<kFp4, R>(sm, P, wk, warp - kValueWarp, lane);
         } else {
             regs_dec<kRegsCopy>();
-            if (warp == kCopyWarp) copy_role<kFp4>(sm, P, wk, lane, &pages_map);
+            if (warp == kCopyWarp) copy_role<kFp4, R>(sm, P, wk, lane, &pages_map);
         }
     }
     __syncthreads();
     if (sm.fail && tid == 0) {   // let the copies in flight finish (bounded), then report
         dev_error(P.err, CSLD_DEVERR_TIMEOUT);
         const int n = sm.n_issued;
-        for (int T = max(0, n - S::kStages); T < n; ++T) (void)mbar_wait(&sm.full[T % S::kStages], (T / S::kStages) & 1);
+        for (int T = max(0, n - kS); T < n; ++T) (void)mbar_wait(&sm.full[T % kS], (T / kS) & 1);
     }
 }
 
@@ -813,7 +921,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid
     __shared__ float4 red[3][kDim / 4];
     __shared__ float2 mls[1024];
     __shared__ int cnt[kMergeThreads / 32], found;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, h = blockIdx.x;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, h = blockIdx.x, n_heads = gridDim.x;   // heads of a row
     pdl_wait();
     pdl_trigger();
     int first = -1;   // the CTA where the y-th cut row begins
@@ -839,13 +947,14 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid
     auto slot = [&](int i) { return 2 * (int64_t)(first + i) + (i == 0 ? 1 : 0); };
     const int d4 = tid % (kDim / 4), g = tid / (kDim / 4);
     const float4* ob = reinterpret_cast<const float4*>(P.opart) + (int64_t)h * (kDim / 4) + d4;
+    const int64_t step = (int64_t)n_heads * (kDim / 4);
     float4 v[kMergeU];
 #pragma unroll
     for (int u = 0; u < kMergeU; ++u) {
         const int i = g + 4 * u;
-        v[u] = i < n ? __ldcg(ob + slot(i) * (kHeads * kDim / 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        v[u] = i < n ? __ldcg(ob + slot(i) * step) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    for (int i = tid; i < n; i += kMergeThreads) mls[i] = __ldcg(&P.mlpart[slot(i) * kHeads + h]);
+    for (int i = tid; i < n; i += kMergeThreads) mls[i] = __ldcg(&P.mlpart[slot(i) * n_heads + h]);
     __syncthreads();
     float M = -INFINITY, L = 0.f;
     for (int i = lane; i < n; i += 32)
@@ -870,11 +979,11 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid
     for (int u = 0; u < kMergeU; ++u)
         if (g + 4 * u < n) add(g + 4 * u, v[u]);
 #pragma unroll 4
-    for (int i = g + 4 * kMergeU; i < n; i += 4) add(i, __ldcg(ob + slot(i) * (kHeads * kDim / 4)));
+    for (int i = g + 4 * kMergeU; i < n; i += 4) add(i, __ldcg(ob + slot(i) * step));
     if (g > 0) red[g - 1][d4] = acc;
     __syncthreads();
     const int64_t row = (static_cast<int64_t>(mt.y) << 32) | static_cast<uint32_t>(mt.x);
-    const int rq = static_cast<int>(row % (P.Q * P.groups)), hh = 16 * (rq % P.groups) + h;
+    const int rq = static_cast<int>(row % P.rows_per_seq), hh = n_heads * (rq % P.row_groups) + h;
     if (g != 0 || hh >= P.heads) return;
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
@@ -884,7 +993,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid
         acc.w += red[k][d4].w;
     }
     const float inv = L == 0.f ? 0.f : 1.f / L;
-    const int64_t at = (row / (P.Q * P.groups) * P.Q + rq / P.groups) * P.heads + hh;
+    const int64_t at = (row / P.rows_per_seq * P.Q + rq / P.row_groups) * P.heads + hh;
     if (P.out_bf16)
         reinterpret_cast<uint2*>(P.out)[at * (kDim / 4) + d4] =
             make_uint2(f32x2_to_bf16x2_bits(acc.x * inv, acc.y * inv), f32x2_to_bf16x2_bits(acc.z * inv, acc.w * inv));
@@ -894,26 +1003,36 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid
 }
 
 namespace {
-constexpr size_t kPartBytes = 2 * kHeads * (kDim * sizeof(float) + sizeof(float2)) + sizeof(int4);   // per CTA
+constexpr int kMaxR = 2;
+constexpr size_t kPartBytes = 2 * kMaxR * kHeads * (kDim * sizeof(float) + sizeof(float2)) + sizeof(int4);   // per CTA
+
+template <bool kFp4, int R>
+cudaError_t launch_rows(const CUtensorMap& map, const Params& P, int num_sms, cudaStream_t stream) {
+    cudaError_t e = set_smem_once(paged_attention_kernel<kFp4, R>, sizeof(Smem<kFp4, R>));
+    if (e != cudaSuccess) return e;
+    return launch_pdl(paged_attention_kernel<kFp4, R>, dim3(num_sms), dim3(kThreads), sizeof(Smem<kFp4, R>), stream, map, P);
 }
+}  // namespace
 
 size_t paged_attention_ws_bytes(int num_sms) { return num_sms * kPartBytes; }
 
 cudaError_t launch_paged_attention(const PagedView& c, bool fp4, const uint16_t* q, int heads, int Q, int W, int sinks,
                                    float scale, void* out, bool out_bf16, float* lse_out, void* ws, int num_sms,
                                    int32_t* err, cudaStream_t stream) {
+    const int R = heads > kHeads ? 2 : 1;   // 16-head groups of a query that a row takes together
     Params P;
     P.c = c;
     P.q = q;
     P.out = out;
     P.lse = lse_out;
     P.opart = static_cast<float*>(ws);
-    P.mlpart = reinterpret_cast<float2*>(P.opart + (size_t)num_sms * 2 * kHeads * kDim);
-    P.meta = reinterpret_cast<int4*>(P.mlpart + (size_t)num_sms * 2 * kHeads);
+    P.mlpart = reinterpret_cast<float2*>(P.opart + (size_t)num_sms * 2 * kMaxR * kHeads * kDim);
+    P.meta = reinterpret_cast<int4*>(P.mlpart + (size_t)num_sms * 2 * kMaxR * kHeads);
     P.err = err;
     P.scale = scale;
     P.heads = heads;
-    P.groups = (heads + kHeads - 1) / kHeads;
+    P.row_groups = (heads + R * kHeads - 1) / (R * kHeads);
+    P.rows_per_seq = Q * P.row_groups;
     P.Q = Q;
     P.W = W;
     P.sinks = sinks;
@@ -922,14 +1041,11 @@ cudaError_t launch_paged_attention(const PagedView& c, bool fp4, const uint16_t*
     CUtensorMap map = {};   // fp8: the pages as rows of 576 bytes
     if (!fp4 && !make_tensor_map_2d_u8(&map, c.pages, kEntry, (uint64_t)c.n_pages * c.page_size, 128, kChunk))
         return cudaErrorInvalidValue;
-    const size_t smem = fp4 ? sizeof(Smem<true>) : sizeof(Smem<false>);
-    auto kernel = fp4 ? paged_attention_kernel<true> : paged_attention_kernel<false>;
-    cudaError_t e = set_smem_once(kernel, smem);
+    cudaError_t e = fp4 ? (R == 2 ? launch_rows<true, 2>(map, P, num_sms, stream) : launch_rows<true, 1>(map, P, num_sms, stream))
+                        : (R == 2 ? launch_rows<false, 2>(map, P, num_sms, stream) : launch_rows<false, 1>(map, P, num_sms, stream));
     if (e != cudaSuccess) return e;
-    e = launch_pdl(kernel, dim3(num_sms), dim3(kThreads), smem, stream, map, P);
-    if (e != cudaSuccess) return e;
-    const int64_t rows = (int64_t)c.batch * Q * P.groups, most = rows < num_sms - 1 ? rows : num_sms - 1;
-    e = launch_pdl(paged_merge_kernel, dim3(kHeads, static_cast<unsigned>(most)), dim3(kMergeThreads), 0, stream, P, num_sms);
+    const int64_t rows = (int64_t)c.batch * P.rows_per_seq, most = rows < num_sms - 1 ? rows : num_sms - 1;
+    e = launch_pdl(paged_merge_kernel, dim3(R * kHeads, static_cast<unsigned>(most)), dim3(kMergeThreads), 0, stream, P, num_sms);
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
 }
