@@ -54,8 +54,8 @@ namespace {
 
 constexpr int kThreads = 640;
 constexpr int kGroupWarps = 4, kScoreWarps = 8, kValueWarp = 8, kValueWarps = 8, kCopyWarp = 16;
-// registers a thread: the launch gives 640 x 96 = 61,440 = 256 x 112 + 256 x 112 + 128 x 32
-constexpr int kRegsScore = 112, kRegsValue = 112, kRegsCopy = 32;
+// registers a thread: the launch gives 640 x 96 = 61,440, these take 256 x 112 + 256 x 104 + 128 x 40 = 60,416
+constexpr int kRegsScore = 112, kRegsValue = 104, kRegsCopy = 40;
 constexpr int kTile = 64, kTileChunks = kTile / kChunk;   // entries per tile; a chunk per warp of a score group
 static_assert(kTileChunks == kGroupWarps, "a group's warp w takes chunk w");
 constexpr int kBlkBytes = kTile * 128;           // one 128-byte column block of a tile
@@ -763,45 +763,49 @@ __device__ __forceinline__ void copy_role(Smem<kFp4, R>& sm, const Params& P, Wa
     constexpr int kS = Smem<kFp4, R>::kStages;
     volatile int32_t* fail = &sm.fail;
     int T = 0;
-    // lane i < 4: chunk i of the tile; its first token and page, loaded one tile ahead
-    auto look = [&](const Walk& w, int t, int& tok, int32_t& pg) {
-        tok = lane < kTileChunks ? w.token_of_chunk((w.t + t) * kTileChunks + lane) : -1;
-        pg = tok >= 0 ? __ldg(P.c.table + (int64_t)w.b * P.c.max_pages + tok / P.c.page_size) : -1;
-    };
     for (; wk.left > 0; wk.next(P)) {
-        int tok, tok1 = -1;
-        int32_t pg, pg1 = -1;
-        look(wk, 0, tok, pg);
-        for (int t = 0; t < wk.len; ++t, ++T) {
-            if (t + 1 < wk.len) look(wk, t + 1, tok1, pg1);
-            const int st = T % kS;
-            bool ok = !*fail;
-            if (T >= kS) ok = ok && wait(&sm.empty[st], (T / kS - 1) & 1, fail);
-            if (!__all_sync(0xffffffffu, ok)) return;
-            if (tok >= 0 && (pg < 0 || pg >= P.c.n_pages)) {
-                dev_error(P.err, CSLD_DEVERR_PAGE);
-                tok = -1;
+        // pages come for kAhead tiles at a time (lane 4 t + i: chunk i of the t-th), the next ones while these are copied
+        constexpr int kAhead = 32 / kTileChunks;
+        auto look = [&](int t, int& tok, int32_t& pg) {
+            tok = wk.token_of_chunk((wk.t + t) * kTileChunks + lane);
+            pg = tok >= 0 ? __ldg(P.c.table + (int64_t)wk.b * P.c.max_pages + tok / P.c.page_size) : -1;
+        };
+        int tok_v, tok_n;
+        int32_t pg_v, pg_n;
+        look(0, tok_n, pg_n);
+        for (int t0 = 0; t0 < wk.len; t0 += kAhead) {
+            tok_v = tok_n;
+            pg_v = pg_n;
+            if (t0 + kAhead < wk.len) look(t0 + kAhead, tok_n, pg_n);
+            if (tok_v >= 0 && (pg_v < 0 || pg_v >= P.c.n_pages)) {
+                if (lane < kTileChunks * (wk.len - t0)) dev_error(P.err, CSLD_DEVERR_PAGE);
+                tok_v = -1;
             }
-            if (lane < kTileChunks) sm.chunk_tok[st][lane] = tok;
-            const int n = __popc(__ballot_sync(0xffffffffu, tok >= 0));
-            __syncwarp();
-            if (lane == 0) {
-                sm.n_issued = T + 1;
-                mbar_arrive_expect_tx(&sm.full[st], n * kChunk * (kFp4 ? kEntry4 : 5 * 128));
+            const int row_v = tok_v >= 0 ? pg_v * P.c.page_size + tok_v % P.c.page_size : 0;   // at most 2^31 - 1 rows
+            const int n_t = min(kAhead, wk.len - t0);
+            for (int t = 0; t < n_t; ++t, ++T) {
+                const int st = T % kS;
+                bool ok = !*fail;
+                if (T >= kS) ok = ok && wait(&sm.empty[st], (T / kS - 1) & 1, fail);
+                if (!__all_sync(0xffffffffu, ok)) return;
+                // fp4: lane i < 4 copies chunk i; fp8: lane 5 i + k column block k of chunk i (a box of 16 rows by 128 bytes)
+                const int ck = kFp4 ? lane : lane / 5, blk = lane % 5, from = kTileChunks * t + min(ck, kTileChunks - 1);
+                const int tok = __shfl_sync(0xffffffffu, tok_v, from), row = __shfl_sync(0xffffffffu, row_v, from);
+                const bool mine = ck < kTileChunks && tok >= 0;
+                if (ck < kTileChunks && (kFp4 || blk == 0)) sm.chunk_tok[st][ck] = tok;
+                const int n = __popc(__ballot_sync(0xffffffffu, mine));
+                if (lane == 0) {
+                    sm.n_issued = T + 1;
+                    mbar_arrive_expect_tx(&sm.full[st], n * (kFp4 ? kChunk4Bytes : kChunk * 128));
+                }
+                __syncwarp();
+                if (mine) {
+                    if constexpr (kFp4)
+                        bulk_g2s(sm.stage[st] + ck * kChunk4Bytes, P.c.pages + (int64_t)row * kEntry4, kChunk4Bytes, &sm.full[st]);
+                    else
+                        tma_load_2d(sm.stage[st] + blk * kBlkBytes + ck * kChunk * 128, pages_map, blk < 4 ? 128 * blk : kNope, row, &sm.full[st]);
+                }
             }
-            __syncwarp();
-            const int64_t row = (int64_t)pg * P.c.page_size + (tok >= 0 ? tok % P.c.page_size : 0);
-            if constexpr (kFp4) {
-                if (tok >= 0) bulk_g2s(sm.stage[st] + lane * kChunk4Bytes, P.c.pages + row * kEntry4, kChunk4Bytes, &sm.full[st]);
-            } else {
-                const int ck = lane / 5, blk = lane % 5;   // one box of 16 rows by 128 bytes a lane
-                const int tk = __shfl_sync(0xffffffffu, tok, ck < kTileChunks ? ck : 0);
-                const int y = __shfl_sync(0xffffffffu, static_cast<int>(row), ck < kTileChunks ? ck : 0);
-                if (ck < kTileChunks && tk >= 0)
-                    tma_load_2d(sm.stage[st] + blk * kBlkBytes + ck * kChunk * 128, pages_map, blk < 4 ? 128 * blk : kNope, y, &sm.full[st]);
-            }
-            tok = tok1;
-            pg = pg1;
         }
     }
 }
