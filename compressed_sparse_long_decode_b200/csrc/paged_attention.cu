@@ -59,7 +59,11 @@ constexpr int kRegsScore = 112, kRegsValue = 104, kRegsCopy = 40;
 constexpr int kTile = 64, kTileChunks = kTile / kChunk;   // entries per tile; a chunk per warp of a score group
 static_assert(kTileChunks == kGroupWarps, "a group's warp w takes chunk w");
 constexpr int kBlkBytes = kTile * 128;           // one 128-byte column block of a tile
-constexpr int kImgBytes = 5 * kBlkBytes;         // dims 0..127, 128..255, 256..383, 384..447, RoPE
+// fp8, as copied: column blocks of dims 0..127, 128..255, 256..383, 384..447 (and half of the RoPE part), RoPE
+constexpr int kTile8Bytes = 5 * kBlkBytes;
+// fp4, as decoded: the same, but for rows of 64 bytes in the block of dims 384..447
+constexpr int kImgBytes = 4 * kBlkBytes + kBlkBytes / 2;
+template <bool kFp4> constexpr int kRopeAt = kFp4 ? 3 * kBlkBytes + kBlkBytes / 2 : 4 * kBlkBytes;
 constexpr int kSteps = kGroups;                  // 32-dim steps of the 448 dims
 constexpr int kQSteps = 2 * kSteps + 4;          // 16-dim MMA steps of the query, the RoPE ones last
 // Marks: a head's nm is set so that the largest p of a tile is 2^kLift and kept until one exceeds 2^kOver.  The
@@ -72,10 +76,11 @@ constexpr int kBarGroup = 1, kBarScore = 3;      // named barriers: the score gr
 
 template <bool kFp4, int R>
 struct Smem {
-    static constexpr int kStages = kFp4 && R == 1 ? 5 : 4;
-    static constexpr int kStageBytes = kFp4 ? kTileChunks * kChunk4Bytes : kImgBytes;
-    uint8_t img[kFp4 ? 2 : 1][kFp4 ? kImgBytes : 1024];   // fp4: value images [block][entry][128 B], 128-byte swizzle
-    uint8_t stage[kStages][kStageBytes];         // fp8: the same layout, as copied
+    static constexpr int kStages = 4;
+    static constexpr int kStageBytes = kFp4 ? kTileChunks * kChunk4Bytes : kTile8Bytes;
+    static constexpr int kImgs = kFp4 ? (R == 1 ? 3 : 2) : 1;   // what fits beside the stages
+    uint8_t stage[kStages][kStageBytes];         // tiles as copied (fp8: multiples of 1024 bytes, for the tensor map's swizzle)
+    uint8_t img[kImgs][kFp4 ? kImgBytes : 16];   // fp4: value images
     uint4 qf[R][kQSteps][32];                    // the query's A fragments
     uint4 p16[2][R][kTileChunks][32];            // P in f16: [chunk][lane] A fragments
     uint4 pbf[2][R][kTileChunks][32];            // bf16 P
@@ -86,7 +91,7 @@ struct Smem {
     float lsum[2][kScoreWarps][R][kHeads], mseg[2][R][kHeads], ginv[2];   // a segment's sums, marks and 1 / g
     int32_t chunk_tok[kStages][kTileChunks];           // first token of a tile's chunks; -1: none
     int32_t resc[2];                             // 0: O stays, 1: O *= f, 2: O = 0 (first tile of a segment)
-    uint64_t full[kStages], empty[kStages], pfull[2], pempty[2], marked[2], segfull[2], segempty[2];
+    uint64_t full[kStages], empty[kStages], imgempty[kImgs], pfull[2], pempty[2], marked[2], segfull[2], segempty[2];
     int64_t red[kThreads / 32], prefix;
     int32_t fail, b0, n_issued;
 };
@@ -197,6 +202,22 @@ struct Walk {
         return i < s.nc ? kChunk * (i < s.cs ? i : s.wl + i - s.cs) : -1;
     }
 };
+// ---- rows in shared memory ---------------------------------------------------------------------
+// A score warp's 16 entries are two MMA column tiles of 8; entry_of: where column col of tile nt lies in the chunk.
+// A row's 16-byte chunks lie at their index XOR a function of the row.  fp8: the 128-byte swizzle of the tensor map
+// (row % 8); fp4: free to choose.  Both are such that the 64-bit accesses of the score warps (four rows at a time,
+// a 32-byte step of each) and the transposing loads of the value warps (eight rows at a time: two columns of either
+// tile, twice) meet every bank once.
+template <bool kFp4>
+__device__ __forceinline__ int entry_of(int nt, int col) {
+    return kFp4 ? 8 * nt + col : 8 * (col >> 2) + 2 * (col & 3) + nt;
+}
+template <bool kFp4>
+__device__ __forceinline__ int swz_wide(int r) { return kFp4 ? ((r & 3) << 1) | ((r >> 3) & 1) : r & 7; }      // 128-byte rows
+__device__ __forceinline__ int swz_half(int r) { return (r & 2) | ((r >> 3) & 1); }                             // fp4: 64-byte rows
+template <bool kFp4>
+__device__ __forceinline__ int swz_rope(int r) { return kFp4 ? ((r & 3) << 1) | ((r >> 2) & 1) : r & 7; }
+
 // ---- numbers --------------------------------------------------------------------------------
 // Eight E2M1 codes (one word) -> eight bytes of the table tab with the codes' signs.
 __device__ __forceinline__ void decode8(uint32_t w, uint2 tab, uint32_t& lo, uint32_t& hi) {
@@ -294,8 +315,19 @@ __device__ __forceinline__ void mma_frag(float (&d)[4], const uint4& a, uint32_t
 // S of this warp's 16 entries, fp4: decodes them (into the value image too).  kFar: some group lies more than 2^26 below
 // its entry's largest, or is NaN.
 template <int R, bool kFar>
-__device__ __forceinline__ void score_fp4(Smem<true, R>& sm, const uint8_t* ch, uint8_t* img, const uint32_t (&at)[4], uint32_t vis,
-                                          int g, int c, int lane, float (&acc)[R][2][2][4]) {
+__device__ __forceinline__ void score_fp4(Smem<true, R>& sm, const uint8_t* ch, uint8_t* img, int w, uint32_t vis, int g, int c, int lane,
+                                          float (&acc)[R][2][2][4]) {
+    // this lane's eight bytes of step s, entry r: row r, chunk 2 (s % 4) + c / 2
+    uint32_t wide[2], half[2], x[4];
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt) {
+        const uint32_t r = 16 * w + 8 * nt + g, b = (((c >> 1) ^ nt) << 4) + 8 * (c & 1);
+        wide[nt] = r * 128 + b;
+        half[nt] = 3 * kBlkBytes + r * 64 + b;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = (i ^ (g & 3)) << 5;
+    const uint32_t xh = ((g >> 1) & 1) << 5;
     int base[2];
     uint32_t tx[2], ty[2], dx[2], dy[2];
 #pragma unroll
@@ -339,7 +371,8 @@ __device__ __forceinline__ void score_fp4(Smem<true, R>& sm, const uint8_t* ch, 
                 if (kFar && dx[nt] && (j < 0 || j > kMaxJ)) tab.x = tab.y = j < 0 ? 0x7F7F7F7Fu : 0u;
                 uint32_t b0, b1;
                 decode8(wd[rd & 1][i][nt], tab, b0, b1);
-                *reinterpret_cast<uint2*>(img + (s >> 2) * kBlkBytes + nt * 1024 + at[s & 3]) = make_uint2(b0, b1);
+                *reinterpret_cast<uint2*>(img + (s < 12 ? (s >> 2) * kBlkBytes + wide[nt] + x[s & 3] : half[nt] + (xh ^ ((s & 1) << 5)))) =
+                    make_uint2(b0, b1);
                 const uint32_t f0 = bytes_to_f16x2<true, 0>(b0), f1 = bytes_to_f16x2<true, 1>(b0);
                 const uint32_t f2 = bytes_to_f16x2<true, 0>(b1), f3 = bytes_to_f16x2<true, 1>(b1);
 #pragma unroll
@@ -351,7 +384,8 @@ __device__ __forceinline__ void score_fp4(Smem<true, R>& sm, const uint8_t* ch, 
     }
 }
 template <int R>
-__device__ __forceinline__ void score_fp8(Smem<false, R>& sm, const uint8_t* img, const uint32_t (&at)[4], int lane, float (&acc)[R][2][2][4]) {
+__device__ __forceinline__ void score_fp8(Smem<false, R>& sm, const uint8_t* img, const uint32_t (&row)[2], const uint32_t (&x)[4], int lane,
+                                          float (&acc)[R][2][2][4]) {
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
         uint4 a[R][2];
@@ -361,7 +395,7 @@ __device__ __forceinline__ void score_fp8(Smem<false, R>& sm, const uint8_t* img
             for (int k = 0; k < 2; ++k) a[r][k] = sm.qf[r][2 * s + k][lane];
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt) {
-            const uint2 b = *reinterpret_cast<const uint2*>(img + (s >> 2) * kBlkBytes + nt * 1024 + at[s & 3]);
+            const uint2 b = *reinterpret_cast<const uint2*>(img + (s >> 2) * kBlkBytes + row[nt] + x[s & 3]);
             const uint32_t f0 = bytes_to_f16x2<false, 0>(b.x), f1 = bytes_to_f16x2<false, 1>(b.x);
             const uint32_t f2 = bytes_to_f16x2<false, 0>(b.y), f3 = bytes_to_f16x2<false, 1>(b.y);
 #pragma unroll
@@ -376,13 +410,19 @@ __device__ __forceinline__ void score_fp8(Smem<false, R>& sm, const uint8_t* img
 template <bool kFp4, int R>
 __device__ __forceinline__ void score_role(Smem<kFp4, R>& sm, const Params& P, Walk wk, int warp, int lane, int64_t u1, int64_t n_cta,
                                            int64_t total) {
-    constexpr int kS = Smem<kFp4, R>::kStages;
+    constexpr int kS = Smem<kFp4, R>::kStages, kI = Smem<kFp4, R>::kImgs;
     volatile int32_t* fail = &sm.fail;
     const int gr = warp >> 2, w = warp & 3, g = lane >> 2, c = lane & 3;   // group gr takes the tiles T % 2 == gr
-    // place of this lane's eight bytes of step s, entry n = 8 nt + g of chunk w: block s / 4, row 16 w + n
-    uint32_t at[4];
+    // this lane's eight bytes of step s of a 128-byte block (RoPE; fp8: all), column g of tile nt: row[nt] + x[s % 4]
+    uint32_t row[2], x32[4];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) at[q] = (16 * w + g) * 128 + ((((c >> 1) ^ g) ^ (2 * q)) << 4) + 8 * (c & 1);
+    for (int nt = 0; nt < 2; ++nt) {
+        const int e = entry_of<kFp4>(nt, g);
+        row[nt] = (16 * w + e) * 128 + (((c >> 1) ^ (swz_rope<kFp4>(e) & 1)) << 4) + 8 * (c & 1);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x32[i] = (i ^ (g & 3)) << 5;   // both tiles: the swizzle's upper bits are g % 4
+    auto mine = [&](int nt, int i) { return entry_of<kFp4>(nt, 2 * c + i); };   // the columns of this lane's scores
     int T = 0, seg = 0;
     for (; wk.left > 0; wk.next(P), ++seg) {
         named_barrier(kBarScore, 32 * kScoreWarps);   // the last row's fragments and marks are done with
@@ -409,9 +449,9 @@ __device__ __forceinline__ void score_role(Smem<kFp4, R>& sm, const Params& P, W
             }
         const int T0 = T, T1 = T + wk.len;
         for (T += (T ^ gr) & 1; T < T1; T += 2) {
-            const int st = T % kS, buf = T & 1;
+            const int st = T % kS, buf = T & 1, im = T % kI;
             bool ok = wait(&sm.full[st], (T / kS) & 1, fail);
-            if (T >= 2) ok = ok && wait(&sm.pempty[buf], ((T >> 1) - 1) & 1, fail);
+            if (kFp4 && T >= kI) ok = ok && wait(&sm.imgempty[im], (T / kI - 1) & 1, fail);
             ok = __all_sync(0xffffffffu, ok);
             const int tok0 = ok ? sm.chunk_tok[st][w] : -1, tk = tok0 + (lane & 15);
             const uint32_t vis = __ballot_sync(0xffffffffu, tok0 >= 0 && tk <= p && (tk > lo || tk < P.sinks)) & 0xFFFFu;
@@ -422,8 +462,8 @@ __device__ __forceinline__ void score_role(Smem<kFp4, R>& sm, const Params& P, W
                 for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) acc[r][nt][0][i] = acc[r][nt][1][i] = racc[r][nt][i] = 0.f;
-            uint8_t* img = kFp4 ? sm.img[kFp4 ? buf : 0] : sm.stage[st];
-            float fe[2][2];   // of the entries 8 nt + 2 c + i: the columns of this lane's scores; 0: masked
+            uint8_t* img = kFp4 ? sm.img[im] : sm.stage[st];
+            float fe[2][2];   // of the entries mine(nt, i); 0: masked
             if constexpr (kFp4) {
                 const uint8_t* ch = sm.stage[st] + w * kChunk4Bytes;
                 // RoPE rows into the image, eight lanes a row
@@ -432,7 +472,7 @@ __device__ __forceinline__ void score_role(Smem<kFp4, R>& sm, const Params& P, W
                     const int en = 4 * i + (lane >> 3), k = lane & 7;
                     uint4 v = *reinterpret_cast<const uint4*>(ch + kChunk4Rope + en * 2 * kRope + 16 * k);
                     if (!((vis >> en) & 1)) v = make_uint4(0, 0, 0, 0);
-                    *reinterpret_cast<uint4*>(img + 4 * kBlkBytes + sw128(16 * w + en, 16 * k)) = v;
+                    *reinterpret_cast<uint4*>(img + kRopeAt<kFp4> + (16 * w + en) * 128 + ((k ^ swz_rope<kFp4>(en)) << 4)) = v;
                 }
                 // groups whose scale lies far below the entry's largest (zero there), or NaN groups (byte 255).  Lane (g, c) looks
                 // at the groups c, c + 4, .. of entries g and 8 + g
@@ -446,19 +486,19 @@ __device__ __forceinline__ void score_role(Smem<kFp4, R>& sm, const Params& P, W
                             most = max(most, static_cast<uint32_t>(base - ch[kChunk4Exp + (4 * s + c) * kChunk + 8 * nt + g]));
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const uint32_t eb = ch[kChunk4Exp + kGroups * kChunk + 8 * nt + 2 * c + i];
-                        fe[nt][i] = (vis >> (8 * nt + 2 * c + i)) & 1 ? __uint_as_float(eb << 23) * 0x1p-13f : 0.f;
+                        const uint32_t eb = ch[kChunk4Exp + kGroups * kChunk + mine(nt, i)];
+                        fe[nt][i] = (vis >> mine(nt, i)) & 1 ? __uint_as_float(eb << 23) * 0x1p-13f : 0.f;
                     }
                 }
-                if (__any_sync(0xffffffffu, most > static_cast<uint32_t>(kMaxJ))) score_fp4<R, true>(sm, ch, img, at, vis, g, c, lane, acc);
-                else score_fp4<R, false>(sm, ch, img, at, vis, g, c, lane, acc);
+                if (__any_sync(0xffffffffu, most > static_cast<uint32_t>(kMaxJ))) score_fp4<R, true>(sm, ch, img, w, vis, g, c, lane, acc);
+                else score_fp4<R, false>(sm, ch, img, w, vis, g, c, lane, acc);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.empty[st]);
             } else {
 #pragma unroll
                 for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) fe[nt][i] = (vis >> (8 * nt + 2 * c + i)) & 1 ? 1.f : 0.f;
+                    for (int i = 0; i < 2; ++i) fe[nt][i] = (vis >> mine(nt, i)) & 1 ? 1.f : 0.f;
                 if (vis != 0xFFFFu) {   // masked rows are zeroed for the value warps
                     for (int en = 0; en < 16; ++en)
                         if (!((vis >> en) & 1))
@@ -467,7 +507,7 @@ __device__ __forceinline__ void score_role(Smem<kFp4, R>& sm, const Params& P, W
                     fence_proxy_async_smem();   // the ring's next copy writes there too
                     __syncwarp();
                 }
-                score_fp8<R>(sm, img, at, lane, acc);
+                score_fp8<R>(sm, img, row, x32, lane, acc);
             }
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
@@ -476,12 +516,12 @@ __device__ __forceinline__ void score_role(Smem<kFp4, R>& sm, const Params& P, W
                 for (int r = 0; r < R; ++r) a[r] = sm.qf[r][2 * kSteps + s][lane];
 #pragma unroll
                 for (int nt = 0; nt < 2; ++nt) {
-                    const uint2 b = *reinterpret_cast<const uint2*>(img + 4 * kBlkBytes + nt * 1024 + at[s]);
+                    const uint2 b = *reinterpret_cast<const uint2*>(img + kRopeAt<kFp4> + row[nt] + x32[s]);
 #pragma unroll
                     for (int r = 0; r < R; ++r) mma_bf16(racc[r][nt], a[r].x, a[r].y, a[r].z, a[r].w, b.x, b.y);
                 }
             }
-            // logits x[r][nt][2 k + i]: entry 8 nt + 2 c + i, head g + 8 k (log2 units), -inf where masked
+            // logits x[r][nt][2 k + i]: entry mine(nt, i), head g + 8 k (log2 units), -inf where masked
             float (&x)[R][2][4] = racc;
             float top[R][2], fmost = fmaxf(fmaxf(fe[0][0], fe[0][1]), fmaxf(fe[1][0], fe[1][1]));
 #pragma unroll
@@ -500,8 +540,9 @@ __device__ __forceinline__ void score_role(Smem<kFp4, R>& sm, const Params& P, W
                             top[r][k] = fmaxf(top[r][k], x[r][nt][n]);
                         }
                 }
-            // the marks, as the tile before left them
+            // the marks, as the tile before left them; the slot of P (and of the factors) is free once its last tile is used
             if (T > 0) (void)wait(&sm.marked[(T - 1) & 1], ((T - 1) >> 1) & 1, fail);
+            if (T >= 2) (void)wait(&sm.pempty[buf], ((T >> 1) - 1) & 1, fail);
             float gs = sm.gs, mk[R][2];
             bool over = kFp4 && fmost * gs > kFeMost;
 #pragma unroll
@@ -562,8 +603,7 @@ __device__ __forceinline__ void score_role(Smem<kFp4, R>& sm, const Params& P, W
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.marked[buf]);
             }
-            // P: p = 2^(x + nm), as A fragments: of the chunk's 16 entries a lane holds 8 nt + 2 c + i, the MMA's k slots
-            // 2c + i (nt = 0) and 2c + 8 + i
+            // P: p = 2^(x + nm), as A fragments: the lane's columns 2c + i are the MMA's k slots 2c + i (nt = 0) and 2c + 8 + i
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 uint32_t pb[2][2], ph[2][2];   // [head][nt]
@@ -625,22 +665,28 @@ __device__ __forceinline__ void score_role(Smem<kFp4, R>& sm, const Params& P, W
 // ---- value warps ---------------------------------------------------------------------------------
 template <bool kFp4, int R>
 __device__ __forceinline__ void value_role(Smem<kFp4, R>& sm, const Params& P, Walk wk, int w, int lane) {
-    constexpr int kS = Smem<kFp4, R>::kStages;
+    constexpr int kS = Smem<kFp4, R>::kStages, kI = Smem<kFp4, R>::kImgs;
     volatile int32_t* fail = &sm.fail;
     const int g = lane >> 2, c = lane & 3;
     const bool rope = w == kValueWarps - 1;
-    // this lane's row address of the matrix loads within a 32-entry block (448 dims) or a 16-entry chunk (RoPE), and
-    // the 16-byte column it starts from
-    int row, col;
+    // this lane's row of the matrix loads, within a 32-entry block (448 dims) or a 16-entry chunk (RoPE); the 16-byte
+    // column that it starts from and its swizzle; bytes from one block or chunk of entries to the next
+    uint32_t off, col, swz, step;
     if (!rope) {
-        const int k = lane & 15, i = k & 3;   // row k of a transposing load (slots 4c + i) -> entry of the chunk lane / 16
-        row = 16 * (lane >> 4) + (i < 2 ? 2 * (k >> 2) + i : 8 + 2 * (k >> 2) + i - 2);
-        col = 4 * (w & 1);
+        const int k = lane & 15, i = k & 3;   // row k of a transposing load: column 2 (k / 4) + i % 2 of tile i / 2
+        const int e = entry_of<kFp4>(i >> 1, 2 * (k >> 2) + (i & 1)), r = 16 * (lane >> 4) + e;
+        const bool half = kFp4 && w == 6;
+        off = (w >> 1) * kBlkBytes + r * (half ? 64 : 128);
+        col = half ? 0 : 4 * (w & 1);
+        swz = half ? swz_half(e) : swz_wide<kFp4>(e);
+        step = half ? 2048 : 4096;
     } else {
-        row = (lane & 7) + 8 * ((lane >> 3) & 1);
+        const int e = entry_of<kFp4>((lane >> 3) & 1, lane & 7);
+        off = kRopeAt<kFp4> + e * 128;
         col = lane >> 4;
+        swz = swz_rope<kFp4>(e);
+        step = 2048;
     }
-    const uint32_t off = (rope ? 4 : w >> 1) * kBlkBytes + (row >> 3) * 1024 + (row & 7) * 128;
     float o[R][8][4];
     int T = 0, seg = 0;
     for (; wk.left > 0; wk.next(P), ++seg) {
@@ -672,7 +718,7 @@ __device__ __forceinline__ void value_role(Smem<kFp4, R>& sm, const Params& P, W
                 }
             }
             if (ok) {
-                const uint32_t base = smem_u32(kFp4 ? sm.img[kFp4 ? buf : 0] : sm.stage[st]) + off;
+                const uint32_t base = smem_u32(kFp4 ? sm.img[T % kI] : sm.stage[st]) + off;
                 if (!rope) {
 #pragma unroll
                     for (int kb = 0; kb < kTile / 32; ++kb) {
@@ -684,7 +730,7 @@ __device__ __forceinline__ void value_role(Smem<kFp4, R>& sm, const Params& P, W
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             uint32_t v[4];   // dims 16 q + lane / 4 (+ 8: odd), chunk 2 kb (+ 1: v[2], v[3])
-                            ldmatrix_b8_trans_x2(v, base + kb * 4096 + (((col + q) ^ (row & 7)) << 4));
+                            ldmatrix_b8_trans_x2(v, base + kb * step + (((col + q) ^ swz) << 4));
 #pragma unroll
                             for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -704,7 +750,7 @@ __device__ __forceinline__ void value_role(Smem<kFp4, R>& sm, const Params& P, W
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             uint32_t v[4];
-                            ldmatrix_b16_trans_x4(v, base + k * 2048 + (((col + 2 * q) ^ (row & 7)) << 4));
+                            ldmatrix_b16_trans_x4(v, base + k * step + (((col + 2 * q) ^ swz) << 4));
 #pragma unroll
                             for (int r = 0; r < R; ++r) {
                                 mma_bf16(o[r][2 * q], a[r].x, a[r].y, a[r].z, a[r].w, v[0], v[1]);
@@ -717,7 +763,7 @@ __device__ __forceinline__ void value_role(Smem<kFp4, R>& sm, const Params& P, W
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(&sm.pempty[buf]);
-                if (!kFp4) mbar_arrive(&sm.empty[st]);
+                mbar_arrive(kFp4 ? &sm.imgempty[T % kI] : &sm.empty[st]);
             }
         }
         // ---- the segment's result ------------------------------------------------------------------
@@ -827,6 +873,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
             mbar_init(&sm.full[s], 1);
             mbar_init(&sm.empty[s], kFp4 ? kGroupWarps : kValueWarps);
         }
+        for (int s = 0; s < S::kImgs; ++s) mbar_init(&sm.imgempty[s], kValueWarps);
         for (int s = 0; s < 2; ++s) {
             mbar_init(&sm.pfull[s], kGroupWarps);
             mbar_init(&sm.pempty[s], kValueWarps);
