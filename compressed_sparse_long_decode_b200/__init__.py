@@ -564,6 +564,10 @@ class PagedCache:
         self._struct = _Paged(code, page_size, self.batch, self.max_pages, self.n_pages, pages.data_ptr(),
                               page_table.data_ptr(), seq_len.data_ptr())
         self._ref = C.byref(self._struct)
+        self._index = pages.get_device()
+
+    def _stream(self):
+        return torch._C._cuda_getCurrentRawStream(self._index)
 
     @classmethod
     def allocate(cls, batch, context, page_size=64, fmt="fp8", device="cuda"):
@@ -578,10 +582,10 @@ class PagedCache:
 
 def _on_device(cache, what, *tensors):
     """The call's tensors lie on the cache's device, and that device is the current one."""
-    if cache.device.index != torch.cuda.current_device():
+    if cache._index != torch._C._cuda_getDevice():
         raise CsldError(f"{what}: the cache is on {cache.device}, the current device is {torch.cuda.current_device()}")
     for t in tensors:
-        if t is not None and t.device != cache.device:
+        if t is not None and t.get_device() != cache._index:
             raise CsldError(f"{what}: a tensor is on {t.device}, the cache on {cache.device}")
 
 
@@ -604,7 +608,7 @@ def kv_cache_append_paged(cache: PagedCache, kv_new, n_new=None, start=None, rop
     # the stride of a dimension of length 1 is never used
     _check(lib.kv_cache_append_paged(cache._ref, kv_new.data_ptr(), kv_new.stride(0) if cache.batch > 1 else 0,
                                      kv_new.stride(1) if T > 1 else 0, T, _ptr(n_new), _ptr(start), rope_base,
-                                     err.data_ptr(), _stream()), "kv_cache_append_paged")
+                                     err.data_ptr(), cache._stream()), "kv_cache_append_paged")
 
 
 def kv_cache_read_paged(cache: PagedCache, start, T, out=None, err=None):
@@ -618,7 +622,7 @@ def kv_cache_read_paged(cache: PagedCache, start, T, out=None, err=None):
         raise CsldError(f"out: expected shape {(cache.batch, T, DIM)}, got {tuple(out.shape)}")
     err = cache.err if err is None else _need(err, torch.int32, "err")
     _on_device(cache, "kv_cache_read_paged", start, out, err)
-    _check(lib.kv_cache_read_paged(cache._ref, start.data_ptr(), T, out.data_ptr(), err.data_ptr(), _stream()),
+    _check(lib.kv_cache_read_paged(cache._ref, start.data_ptr(), T, out.data_ptr(), err.data_ptr(), cache._stream()),
            "kv_cache_read_paged")
     return out
 
@@ -649,7 +653,7 @@ def _paged_attention(what, call, cache, q, scale, out, lse, ws, err, *masks):
     err = cache.err if err is None else _need(err, torch.int32, "err")
     _on_device(cache, what, q, out, lse, ws, err)
     _check(call(cache._ref, q.data_ptr(), heads, Q, *masks, scale, out.data_ptr(), int(out.dtype == torch.bfloat16),
-                lse.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), err.data_ptr(), _stream()), what)
+                lse.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), err.data_ptr(), cache._stream()), what)
     return out, lse
 
 

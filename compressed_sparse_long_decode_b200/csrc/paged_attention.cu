@@ -54,8 +54,11 @@ namespace {
 
 constexpr int kThreads = 640;
 constexpr int kGroupWarps = 4, kScoreWarps = 8, kValueWarp = 8, kValueWarps = 8, kCopyWarp = 16;
-// registers a thread: the launch gives 640 x 96 = 61,440, these take 256 x 112 + 256 x 104 + 128 x 40 = 60,416
-constexpr int kRegsScore = 112, kRegsValue = 104, kRegsCopy = 40;
+// registers a thread: the launch gives 640 x 96 = 61,440; R = 1 takes 256 x 112 + 256 x 104 + 128 x 40 = 60,416 of
+// them, R = 2 256 x 120 + 256 x 104 + 128 x 32 = 61,440
+template <int R> constexpr int kRegsScore = R == 1 ? 112 : 120;
+constexpr int kRegsValue = 104;
+template <int R> constexpr int kRegsCopy = R == 1 ? 40 : 32;
 constexpr int kTile = 64, kTileChunks = kTile / kChunk;   // entries per tile; a chunk per warp of a score group
 static_assert(kTileChunks == kGroupWarps, "a group's warp w takes chunk w");
 constexpr int kBlkBytes = kTile * 128;           // one 128-byte column block of a tile
@@ -108,8 +111,8 @@ struct Params {
     int4* meta;          // [CTAs]: (row low, row high, last CTA, -) of the cut row that begins there; last CTA -1: none
     int32_t* err;
     float scale;
-    int heads, rows_per_seq, row_groups, Q, W, sinks, min_tiles;   // row_groups: rows per query
-    bool out_bf16;
+    int heads, rows_per_seq, row_groups, Q, W, sinks;   // row_groups: rows per query
+    bool out_bf16, whole;   // whole: shares are whole rows
 };
 
 // Bounded wait: false once any wait of the CTA has given up (this one after about a second).
@@ -130,10 +133,25 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, i
         "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
         :: "r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar)) : "memory");
 }
-__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+template <bool kZero>   // kZero: d is overwritten
+__device__ __forceinline__ void mma_bf16_frag(float (&d)[4], const uint4& a, uint32_t b0, uint32_t b1) {
+    if constexpr (kZero)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3]) : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1), "f"(0.f));
+    else
+        mma_bf16(d, a.x, a.y, a.z, a.w, b0, b1);
+}
+template <bool kZero>
+__device__ __forceinline__ void mma_f16_frag(float (&d)[4], const uint4& a, uint32_t b0, uint32_t b1) {
+    if constexpr (kZero)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3]) : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1), "f"(0.f));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
 }
 // Two 16 x 16 byte matrices, transposed: lane i gives the address of row i (16 B).  r0, r2: bytes of rows 4 (lane % 4)
 // .. + 3 of the first and second matrix at column lane / 4; r1, r3: at column 8 + lane / 4.
@@ -178,25 +196,31 @@ __device__ __forceinline__ SeqInfo seq_info(const Params& P, int b) {
 // A CTA's walk over its share, segment by segment; every role walks it by itself.
 struct Walk {
     int b, rq, t;        // sequence, row within it, first tile of the segment
-    int left, len;       // tiles left in the share (this segment included), tiles of this segment
+    int left, len;       // tiles (whole rows: rows) left in the share, this segment included; tiles of this segment
     SeqInfo s;
-    __device__ __forceinline__ void begin(const Params& P, int b_, int64_t off, int n_tiles) {
+    __device__ __forceinline__ void begin(const Params& P, int b_, int64_t off, int n) {
         b = b_;
         s = seq_info(P, b);
+        left = n;
+        if (P.whole) {
+            rq = static_cast<int>(off);
+            t = 0;
+            len = s.tiles;
+            return;
+        }
         rq = static_cast<int>(off / s.tiles);
         t = static_cast<int>(off % s.tiles);
-        left = n_tiles;
         len = min(s.tiles - t, left);
     }
     __device__ __forceinline__ void next(const Params& P) {
-        left -= len;
+        left -= P.whole ? 1 : len;
         t = 0;
         if (left <= 0) return;
         if (++rq == P.rows_per_seq) {
             rq = 0;
             s = seq_info(P, ++b);
         }
-        len = min(s.tiles, left);
+        len = P.whole ? s.tiles : min(s.tiles, left);
     }
     __device__ __forceinline__ int token_of_chunk(int i) const {   // i: chunk of the row's list
         return i < s.nc ? kChunk * (i < s.cs ? i : s.wl + i - s.cs) : -1;
@@ -306,12 +330,6 @@ __device__ __forceinline__ void build_fragments(Smem<kFp4, R>& sm, const Params&
 }
 
 // ---- score warps ---------------------------------------------------------------------------------
-// One MMA of f16 (or, for the RoPE steps, bf16) with an A fragment from shared memory.
-__device__ __forceinline__ void mma_frag(float (&d)[4], const uint4& a, uint32_t b0, uint32_t b1) {
-    const uint32_t f[4] = {a.x, a.y, a.z, a.w};
-    mma_f16(d, f, b0, b1);
-}
-
 // S of this warp's 16 entries, fp4: decodes them (into the value image too).  kFar: some group lies more than 2^26 below
 // its entry's largest, or is NaN.
 template <int R, bool kFar>
@@ -377,8 +395,13 @@ __device__ __forceinline__ void score_fp4(Smem<true, R>& sm, const uint8_t* ch, 
                 const uint32_t f2 = bytes_to_f16x2<true, 0>(b1), f3 = bytes_to_f16x2<true, 1>(b1);
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
-                    mma_frag(acc[r][nt][0], a[r][2 * i], f0, f1);
-                    mma_frag(acc[r][nt][1], a[r][2 * i + 1], f2, f3);
+                    if (s == 0) {
+                        mma_f16_frag<true>(acc[r][nt][0], a[r][2 * i], f0, f1);
+                        mma_f16_frag<true>(acc[r][nt][1], a[r][2 * i + 1], f2, f3);
+                    } else {
+                        mma_f16_frag<false>(acc[r][nt][0], a[r][2 * i], f0, f1);
+                        mma_f16_frag<false>(acc[r][nt][1], a[r][2 * i + 1], f2, f3);
+                    }
                 }
             }
     }
@@ -400,8 +423,13 @@ __device__ __forceinline__ void score_fp8(Smem<false, R>& sm, const uint8_t* img
             const uint32_t f2 = bytes_to_f16x2<false, 0>(b.y), f3 = bytes_to_f16x2<false, 1>(b.y);
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                mma_frag(acc[r][nt][0], a[r][0], f0, f1);
-                mma_frag(acc[r][nt][1], a[r][1], f2, f3);
+                if (s == 0) {
+                    mma_f16_frag<true>(acc[r][nt][0], a[r][0], f0, f1);
+                    mma_f16_frag<true>(acc[r][nt][1], a[r][1], f2, f3);
+                } else {
+                    mma_f16_frag<false>(acc[r][nt][0], a[r][0], f0, f1);
+                    mma_f16_frag<false>(acc[r][nt][1], a[r][1], f2, f3);
+                }
             }
         }
     }
@@ -456,12 +484,6 @@ __device__ __forceinline__ void score_role(Smem<kFp4, R>& sm, const Params& P, W
             const int tok0 = ok ? sm.chunk_tok[st][w] : -1, tk = tok0 + (lane & 15);
             const uint32_t vis = __ballot_sync(0xffffffffu, tok0 >= 0 && tk <= p && (tk > lo || tk < P.sinks)) & 0xFFFFu;
             float acc[R][2][2][4], racc[R][2][4];   // [entries 8 nt ..][half of a step: independent chains]; RoPE part
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-#pragma unroll
-                for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[r][nt][0][i] = acc[r][nt][1][i] = racc[r][nt][i] = 0.f;
             uint8_t* img = kFp4 ? sm.img[im] : sm.stage[st];
             float fe[2][2];   // of the entries mine(nt, i); 0: masked
             if constexpr (kFp4) {
@@ -518,7 +540,10 @@ __device__ __forceinline__ void score_role(Smem<kFp4, R>& sm, const Params& P, W
                 for (int nt = 0; nt < 2; ++nt) {
                     const uint2 b = *reinterpret_cast<const uint2*>(img + kRopeAt<kFp4> + row[nt] + x32[s]);
 #pragma unroll
-                    for (int r = 0; r < R; ++r) mma_bf16(racc[r][nt], a[r].x, a[r].y, a[r].z, a[r].w, b.x, b.y);
+                    for (int r = 0; r < R; ++r) {
+                        if (s == 0) mma_bf16_frag<true>(racc[r][nt], a[r], b.x, b.y);
+                        else mma_bf16_frag<false>(racc[r][nt], a[r], b.x, b.y);
+                    }
                 }
             }
             // logits x[r][nt][2 k + i]: entry mine(nt, i), head g + 8 k (log2 units), -inf where masked
@@ -737,7 +762,7 @@ __device__ __forceinline__ void value_role(Smem<kFp4, R>& sm, const Params& P, W
                                 for (int n = 0; n < 2; ++n) {
                                     const uint32_t b0 = bytes_to_f16x2<kFp4, 0>(v[2 * u + n]), b1 = bytes_to_f16x2<kFp4, 1>(v[2 * u + n]);
 #pragma unroll
-                                    for (int r = 0; r < R; ++r) mma_frag(o[r][2 * q + n], a[r][u], b0, b1);
+                                    for (int r = 0; r < R; ++r) mma_f16_frag<false>(o[r][2 * q + n], a[r][u], b0, b1);
                                 }
                         }
                     }
@@ -753,8 +778,8 @@ __device__ __forceinline__ void value_role(Smem<kFp4, R>& sm, const Params& P, W
                             ldmatrix_b16_trans_x4(v, base + k * step + (((col + 2 * q) ^ swz) << 4));
 #pragma unroll
                             for (int r = 0; r < R; ++r) {
-                                mma_bf16(o[r][2 * q], a[r].x, a[r].y, a[r].z, a[r].w, v[0], v[1]);
-                                mma_bf16(o[r][2 * q + 1], a[r].x, a[r].y, a[r].z, a[r].w, v[2], v[3]);
+                                mma_bf16_frag<false>(o[r][2 * q], a[r], v[0], v[1]);
+                                mma_bf16_frag<false>(o[r][2 * q + 1], a[r], v[2], v[3]);
                             }
                         }
                     }
@@ -810,6 +835,10 @@ __device__ __forceinline__ void copy_role(Smem<kFp4, R>& sm, const Params& P, Wa
     volatile int32_t* fail = &sm.fail;
     int T = 0;
     for (; wk.left > 0; wk.next(P)) {
+        if (lane == 0) {
+            const int32_t n = P.c.seq_len[wk.b];
+            if (n < 0 || n > P.c.capacity()) dev_error(P.err, CSLD_DEVERR_SEQ_LEN);
+        }
         // pages come for kAhead tiles at a time (lane 4 t + i: chunk i of the t-th), the next ones while these are copied
         constexpr int kAhead = 32 / kTileChunks;
         auto look = [&](int t, int& tok, int32_t& pg) {
@@ -889,71 +918,79 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
     pdl_wait();
     pdl_trigger();
 
-    // ---- this CTA's share of all rows' tiles ------------------------------------------------------
+    // ---- this CTA's share -------------------------------------------------------------------------
     const int rows_per_seq = P.rows_per_seq;
-    int64_t mine = 0;
-    for (int b = tid; b < P.c.batch; b += kThreads) {
-        const int32_t n = P.c.seq_len[b];
-        if ((n < 0 || n > P.c.capacity()) && blockIdx.x == 0) dev_error(P.err, CSLD_DEVERR_SEQ_LEN);
-        mine += seq_info(P, b).tiles;
-    }
-    auto block_scan = [&](int64_t v, int64_t& total) {   // exclusive prefix of v over the threads
-        int64_t inc = v;
+    int64_t total = 0, n_cta = gridDim.x, u1 = 0, first = 0;   // of split rows: all tiles, CTAs with a share, its end; its begin
+    int b0, n_units;
+    if (P.whole) {
+        const int64_t rows = (int64_t)P.c.batch * rows_per_seq, r0 = rows * blockIdx.x / n_cta;
+        n_units = static_cast<int>(rows * (blockIdx.x + 1) / n_cta - r0);
+        b0 = static_cast<int>(r0 / rows_per_seq);
+        first = r0 % rows_per_seq;
+        __syncthreads();
+    } else {
+        int64_t mine = 0;
+        for (int b = tid; b < P.c.batch; b += kThreads) mine += seq_info(P, b).tiles;
+        auto block_scan = [&](int64_t v, int64_t& sum) {   // exclusive prefix of v over the threads
+            int64_t inc = v;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += y;
-        }
-        __syncthreads();
-        if (lane == 31) sm.red[warp] = inc;
-        __syncthreads();
-        int64_t before = 0;
-        total = 0;
-        for (int w = 0; w < kThreads / 32; ++w) {
-            if (w < warp) before += sm.red[w];
-            total += sm.red[w];
-        }
-        return before + inc - v;
-    };
-    int64_t all;
-    const int64_t pre = block_scan(mine, all);
-    const int64_t total = all * rows_per_seq;
-    const int64_t n_cta = max64(1, min64((int64_t)gridDim.x, total / P.min_tiles));
-    const int64_t u0 = blockIdx.x < n_cta ? total * blockIdx.x / n_cta : 0;
-    const int64_t u1 = blockIdx.x < n_cta ? total * (blockIdx.x + 1) / n_cta : 0;
-    const int n_tiles = static_cast<int>(u1 - u0);
-    if (n_tiles > 0) {   // the sequence that the share begins in
-        int64_t base = 0;
-        for (int b1 = 0; b1 < P.c.batch; b1 += kThreads) {
-            int64_t v, p, tot;
-            if (P.c.batch <= kThreads) {
-                v = mine;
-                p = pre;
-                tot = all;
-            } else {
-                v = b1 + tid < P.c.batch ? seq_info(P, b1 + tid).tiles : 0;
-                p = block_scan(v, tot) + base;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += y;
             }
-            if (v > 0 && p * rows_per_seq <= u0 && u0 < (p + v) * rows_per_seq) {
-                sm.b0 = b1 + tid;
-                sm.prefix = p * rows_per_seq;
+            __syncthreads();
+            if (lane == 31) sm.red[warp] = inc;
+            __syncthreads();
+            int64_t before = 0;
+            sum = 0;
+            for (int w = 0; w < kThreads / 32; ++w) {
+                if (w < warp) before += sm.red[w];
+                sum += sm.red[w];
             }
-            base += tot;
+            return before + inc - v;
+        };
+        int64_t all;
+        const int64_t pre = block_scan(mine, all);
+        total = all * rows_per_seq;
+        n_cta = min64(n_cta, total);
+        const int64_t u0 = blockIdx.x < n_cta ? total * blockIdx.x / n_cta : 0;
+        u1 = blockIdx.x < n_cta ? total * (blockIdx.x + 1) / n_cta : 0;
+        n_units = static_cast<int>(u1 - u0);
+        if (n_units > 0) {   // the sequence that the share begins in
+            int64_t base = 0;
+            for (int b1 = 0; b1 < P.c.batch; b1 += kThreads) {
+                int64_t v, p, tot;
+                if (P.c.batch <= kThreads) {
+                    v = mine;
+                    p = pre;
+                    tot = all;
+                } else {
+                    v = b1 + tid < P.c.batch ? seq_info(P, b1 + tid).tiles : 0;
+                    p = block_scan(v, tot) + base;
+                }
+                if (v > 0 && p * rows_per_seq <= u0 && u0 < (p + v) * rows_per_seq) {
+                    sm.b0 = b1 + tid;
+                    sm.prefix = p * rows_per_seq;
+                }
+                base += tot;
+            }
         }
+        if (tid == 0) P.meta[blockIdx.x] = make_int4(0, 0, -1, 0);   // overwritten by this thread where a cut row begins
+        __syncthreads();
+        b0 = sm.b0;
+        first = u0 - sm.prefix;
     }
-    if (tid == 0) P.meta[blockIdx.x] = make_int4(0, 0, -1, 0);   // overwritten by this thread where a cut row begins
-    __syncthreads();
-    if (n_tiles > 0) {
+    if (n_units > 0) {
         Walk wk;
-        wk.begin(P, sm.b0, u0 - sm.prefix, n_tiles);
+        wk.begin(P, b0, first, n_units);
         if (warp < kScoreWarps) {
-            regs_inc<kRegsScore>();
+            regs_inc<kRegsScore<R>>();
             score_role<kFp4, R>(sm, P, wk, warp, lane, u1, n_cta, total);
         } else if (warp < kValueWarp + kValueWarps) {
             regs_inc<kRegsValue>();
             value_role<kFp4, R>(sm, P, wk, warp - kValueWarp, lane);
         } else {
-            regs_dec<kRegsCopy>();
+            regs_dec<kRegsCopy<R>>();
             if (warp == kCopyWarp) copy_role<kFp4, R>(sm, P, wk, lane, &pages_map);
         }
     }
@@ -1055,13 +1092,14 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid
 
 namespace {
 constexpr int kMaxR = 2;
+constexpr int kMergeTiles = 4;   // what cutting rows costs, in tiles of a CTA's time: the scan of lengths and the merge launch
 constexpr size_t kPartBytes = 2 * kMaxR * kHeads * (kDim * sizeof(float) + sizeof(float2)) + sizeof(int4);   // per CTA
 
 template <bool kFp4, int R>
-cudaError_t launch_rows(const CUtensorMap& map, const Params& P, int num_sms, cudaStream_t stream) {
+cudaError_t launch_rows(const CUtensorMap& map, const Params& P, int n_cta, cudaStream_t stream) {
     cudaError_t e = set_smem_once(paged_attention_kernel<kFp4, R>, sizeof(Smem<kFp4, R>));
     if (e != cudaSuccess) return e;
-    return launch_pdl(paged_attention_kernel<kFp4, R>, dim3(num_sms), dim3(kThreads), sizeof(Smem<kFp4, R>), stream, map, P);
+    return launch_pdl(paged_attention_kernel<kFp4, R>, dim3(n_cta), dim3(kThreads), sizeof(Smem<kFp4, R>), stream, map, P);
 }
 }  // namespace
 
@@ -1087,15 +1125,23 @@ cudaError_t launch_paged_attention(const PagedView& c, bool fp4, const uint16_t*
     P.Q = Q;
     P.W = W;
     P.sinks = sinks;
-    P.min_tiles = 1;
     P.out_bf16 = out_bf16;
     CUtensorMap map = {};   // fp8: the pages as rows of 576 bytes
     if (!fp4 && !make_tensor_map_2d_u8(&map, c.pages, kEntry, (uint64_t)c.n_pages * c.page_size, 128, kChunk))
         return cudaErrorInvalidValue;
-    cudaError_t e = fp4 ? (R == 2 ? launch_rows<true, 2>(map, P, num_sms, stream) : launch_rows<true, 1>(map, P, num_sms, stream))
-                        : (R == 2 ? launch_rows<false, 2>(map, P, num_sms, stream) : launch_rows<false, 1>(map, P, num_sms, stream));
+    // Whole rows or cut ones.  The longest row has t tiles, as far as the host knows (the window, or the capacity).
+    const int64_t rows = (int64_t)c.batch * P.rows_per_seq;
+    int64_t chunks = (c.capacity() + kChunk - 1) / kChunk;
+    if (W > 0) chunks = min64(chunks, (min64(sinks, c.capacity()) + kChunk - 1) / kChunk + (min64(W, c.capacity()) + Q - 1 + 2 * kChunk - 2) / kChunk);
+    const int64_t t = (chunks + kTileChunks - 1) / kTileChunks, n_cta = min64(num_sms, rows);
+    P.whole = (rows + n_cta - 1) / n_cta * t <= rows * t / num_sms + kMergeTiles;
+    cudaError_t e = fp4 ? (R == 2 ? launch_rows<true, 2>(map, P, P.whole ? n_cta : num_sms, stream)
+                                  : launch_rows<true, 1>(map, P, P.whole ? n_cta : num_sms, stream))
+                        : (R == 2 ? launch_rows<false, 2>(map, P, P.whole ? n_cta : num_sms, stream)
+                                  : launch_rows<false, 1>(map, P, P.whole ? n_cta : num_sms, stream));
     if (e != cudaSuccess) return e;
-    const int64_t rows = (int64_t)c.batch * P.rows_per_seq, most = rows < num_sms - 1 ? rows : num_sms - 1;
+    if (P.whole) return cudaGetLastError();
+    const int64_t most = rows < num_sms - 1 ? rows : num_sms - 1;
     e = launch_pdl(paged_merge_kernel, dim3(R * kHeads, static_cast<unsigned>(most)), dim3(kMergeThreads), 0, stream, P, num_sms);
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
