@@ -75,7 +75,12 @@ constexpr int kQSteps = 2 * kSteps + 4;          // 16-dim MMA steps of the quer
 template <bool kFp4> constexpr float kLift = kFp4 ? 0.f : 5.f;
 template <bool kFp4> constexpr float kOver = kFp4 ? 10.f : 15.f;
 constexpr float kFeSet = 8.f, kFeMost = 32.f, kUnset = 1e30f;
-constexpr int kBarGroup = 1, kBarScore = 3;      // named barriers: the score groups' (1, 2), both groups' (3)
+// hardware barriers: the score groups' own (1, 2), both groups' (3); from a group to the value warps: P of a tile is there
+// (4, 5), back: its slot is free (6, 7), a value image is free (8, 9, 10); from group to group: the marks are there (11,
+// 12); from the score to the value warps: a segment's sums (13), back: taken (14)
+constexpr int kBarGroup = 1, kBarScore = 3, kBarP = 4, kBarPFree = 6, kBarImg = 8, kBarMark = 11, kBarSeg = 13, kBarSegFree = 14;
+constexpr int kGroupThreads = 32 * kGroupWarps, kScoreThreads = 32 * kScoreWarps, kValueThreads = 32 * kValueWarps;
+constexpr int kHandover = kGroupThreads + kValueThreads;
 
 template <bool kFp4, int R>
 struct Smem {
@@ -91,10 +96,10 @@ struct Smem {
     float c2[R][kHeads], sq[R][kHeads];          // logit factors (log2 units), scales of the query
     float nm[R][kHeads], gs;                     // the marks
     float tmax[2][kGroupWarps][R][kHeads], femax[2][kGroupWarps];
-    float lsum[2][kScoreWarps][R][kHeads], mseg[2][R][kHeads], ginv[2];   // a segment's sums, marks and 1 / g
+    float lsum[kScoreWarps][R][kHeads], mseg[R][kHeads], ginv;   // a segment's sums, marks and 1 / g
     int32_t chunk_tok[kStages][kTileChunks];           // first token of a tile's chunks; -1: none
     int32_t resc[2];                             // 0: O stays, 1: O *= f, 2: O = 0 (first tile of a segment)
-    uint64_t full[kStages], empty[kStages], imgempty[kImgs], pfull[2], pempty[2], marked[2], segfull[2], segempty[2];
+    uint64_t full[kStages], empty[kStages];
     int64_t red[kThreads / 32], prefix;
     int32_t fail, b0, n_issued;
 };
@@ -115,17 +120,30 @@ struct Params {
     bool out_bf16, whole;   // whole: shares are whole rows
 };
 
-// Bounded wait: false once any wait of the CTA has given up (this one after about a second).
+// Bounded wait for a copy or a ring slot: false once any such wait of the CTA has given up (this one after about a
+// second).  Only these poll.  The roles hand work to one another through hardware barriers (below), where a waiting
+// warp takes no issue slots: with mbarriers there too, polls were 35 % of all instructions.
+template <bool kSleep>
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int32_t* fail) {
     for (uint32_t i = 0; i < (1u << 22); ++i) {
         if (mbar_try_wait(bar, parity)) return true;
-        if (i >= 16) {
+        if (kSleep || i >= 16) {
             if (*fail) return false;
-            __nanosleep(64);
+            __nanosleep(kSleep ? 100 : 64);
         }
     }
     *fail = 1;
     return false;
+}
+// Producer and consumer sides of a hardware barrier of n threads in all.  Every arrival of one use is met by exactly one
+// sync, in the failure path too (a role that gives up on a copy goes on through its barriers).
+__device__ __forceinline__ void bar_arrive(int id, int n) {
+    __syncwarp();
+    asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(n) : "memory");
+}
+__device__ __forceinline__ void bar_sync(int id, int n) {
+    __syncwarp();
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
 }
 __device__ __forceinline__ float pow2f(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
@@ -453,7 +471,7 @@ __device__ __forceinline__ void score_role(Smem<kFp4, R>& sm, const Params& P, W
     auto mine = [&](int nt, int i) { return entry_of<kFp4>(nt, 2 * c + i); };   // the columns of this lane's scores
     int T = 0, seg = 0;
     for (; wk.left > 0; wk.next(P), ++seg) {
-        named_barrier(kBarScore, 32 * kScoreWarps);   // the last row's fragments and marks are done with
+        named_barrier(kBarScore, kScoreThreads);   // the last row's fragments and marks are done with
         scale_query<kFp4, R>(sm, P, wk.b, wk.rq, warp, lane);
         if (warp == 0) {
             if (lane < kHeads)
@@ -461,9 +479,9 @@ __device__ __forceinline__ void score_role(Smem<kFp4, R>& sm, const Params& P, W
                 for (int r = 0; r < R; ++r) sm.nm[r][lane] = kUnset;
             if (lane == 0) sm.gs = 0.f;   // not set yet
         }
-        named_barrier(kBarScore, 32 * kScoreWarps);
+        named_barrier(kBarScore, kScoreThreads);
         build_fragments<kFp4, R>(sm, P, wk.b, wk.rq, warp, lane);
-        named_barrier(kBarScore, 32 * kScoreWarps);
+        named_barrier(kBarScore, kScoreThreads);
         const int p = wk.s.n - P.Q + wk.rq / P.row_groups;   // the query's position; it sees t <= p, t > lo or t < sinks
         const int lo = P.W > 0 ? max(p, 0) - P.W : -1;
         float nm[R][2], l[R][2], c2[R][2];   // heads g, g + 8; l is relative to nm
@@ -478,9 +496,8 @@ __device__ __forceinline__ void score_role(Smem<kFp4, R>& sm, const Params& P, W
         const int T0 = T, T1 = T + wk.len;
         for (T += (T ^ gr) & 1; T < T1; T += 2) {
             const int st = T % kS, buf = T & 1, im = T % kI;
-            bool ok = wait(&sm.full[st], (T / kS) & 1, fail);
-            if (kFp4 && T >= kI) ok = ok && wait(&sm.imgempty[im], (T / kI - 1) & 1, fail);
-            ok = __all_sync(0xffffffffu, ok);
+            const bool ok = __all_sync(0xffffffffu, wait<false>(&sm.full[st], (T / kS) & 1, fail));
+            if (kFp4 && T >= kI) bar_sync(kBarImg + im, kHandover);
             const int tok0 = ok ? sm.chunk_tok[st][w] : -1, tk = tok0 + (lane & 15);
             const uint32_t vis = __ballot_sync(0xffffffffu, tok0 >= 0 && tk <= p && (tk > lo || tk < P.sinks)) & 0xFFFFu;
             float acc[R][2][2][4], racc[R][2][4];   // [entries 8 nt ..][half of a step: independent chains]; RoPE part
@@ -566,8 +583,8 @@ __device__ __forceinline__ void score_role(Smem<kFp4, R>& sm, const Params& P, W
                         }
                 }
             // the marks, as the tile before left them; the slot of P (and of the factors) is free once its last tile is used
-            if (T > 0) (void)wait(&sm.marked[(T - 1) & 1], ((T - 1) >> 1) & 1, fail);
-            if (T >= 2) (void)wait(&sm.pempty[buf], ((T >> 1) - 1) & 1, fail);
+            if (T > T0) bar_sync(kBarMark + ((T - 1) & 1), kScoreThreads);
+            if (T >= 2) bar_sync(kBarPFree + buf, kHandover);
             float gs = sm.gs, mk[R][2];
             bool over = kFp4 && fmost * gs > kFeMost;
 #pragma unroll
@@ -578,7 +595,7 @@ __device__ __forceinline__ void score_role(Smem<kFp4, R>& sm, const Params& P, W
                     over |= top[r][k] + mk[r][k] > kOver<kFp4>;
                 }
             int resc = T == T0 ? 2 : 0;
-            if (named_barrier_or(kBarGroup + gr, 32 * kGroupWarps, over)) {
+            if (named_barrier_or(kBarGroup + gr, kGroupThreads, over)) {
                 // some weight is too large, or the first tile: the tile's maxima; a head that lies more than 2 above its
                 // mark gets a new one, and the value warps the factors of what they hold
 #pragma unroll
@@ -593,7 +610,7 @@ __device__ __forceinline__ void score_role(Smem<kFp4, R>& sm, const Params& P, W
                     const uint32_t fm = __reduce_max_sync(0xffffffffu, __float_as_uint(fmost));
                     if (lane == 0) sm.femax[gr][w] = __uint_as_float(fm);
                 }
-                named_barrier(kBarGroup + gr, 32 * kGroupWarps);
+                named_barrier(kBarGroup + gr, kGroupThreads);
                 float fg = 1.f;
                 if constexpr (kFp4) {
                     const float fm = fmaxf(fmaxf(sm.femax[gr][0], sm.femax[gr][1]), fmaxf(sm.femax[gr][2], sm.femax[gr][3]));
@@ -624,10 +641,7 @@ __device__ __forceinline__ void score_role(Smem<kFp4, R>& sm, const Params& P, W
                 if (w == 0 && lane == 0) sm.gs = gs;
                 if (T > T0) resc = 1;
             }
-            if (w == 0) {
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.marked[buf]);
-            }
+            bar_arrive(kBarMark + buf, kScoreThreads);
             // P: p = 2^(x + nm), as A fragments: the lane's columns 2c + i are the MMA's k slots 2c + i (nt = 0) and 2c + 8 + i
 #pragma unroll
             for (int r = 0; r < R; ++r) {
@@ -650,14 +664,12 @@ __device__ __forceinline__ void score_role(Smem<kFp4, R>& sm, const Params& P, W
                 sm.pbf[buf][r][w][lane] = make_uint4(pb[0][0], pb[1][0], pb[0][1], pb[1][1]);
             }
             if (w == 0 && lane == 0) sm.resc[buf] = resc;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.pfull[buf]);
+            bar_arrive(kBarP + buf, kHandover);
         }
         T = T1;
         // ---- the segment's sums, relative to the last marks --------------------------------------------
-        const int sb = seg & 1;
-        (void)wait(&sm.marked[(T1 - 1) & 1], ((T1 - 1) >> 1) & 1, fail);
-        if (seg >= 2) (void)wait(&sm.segempty[sb], ((seg >> 1) - 1) & 1, fail);
+        if (((T1 - 1) & 1) != gr) bar_sync(kBarMark + ((T1 - 1) & 1), kScoreThreads);
+        if (seg >= 1) bar_sync(kBarSegFree, kScoreThreads + kValueThreads);
 #pragma unroll
         for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -667,12 +679,12 @@ __device__ __forceinline__ void score_role(Smem<kFp4, R>& sm, const Params& P, W
                 v += __shfl_xor_sync(0xffffffffu, v, 1);
                 v += __shfl_xor_sync(0xffffffffu, v, 2);
                 if (c == 0) {
-                    sm.lsum[sb][warp][r][g + 8 * k] = v;
-                    if (warp == 0) sm.mseg[sb][r][g + 8 * k] = -mk;
+                    sm.lsum[warp][r][g + 8 * k] = v;
+                    if (warp == 0) sm.mseg[r][g + 8 * k] = -mk;
                 }
             }
         if (warp == 0 && lane == 0) {
-            sm.ginv[sb] = sm.gs != 0.f ? 1.f / sm.gs : 1.f;
+            sm.ginv = sm.gs != 0.f ? 1.f / sm.gs : 1.f;
             if (wk.t == 0 && wk.len < wk.s.tiles) {   // a cut row begins here: which CTA holds its end
                 const int64_t row = (int64_t)wk.b * P.rows_per_seq + wk.rq;
                 const int64_t end = u1 - wk.left + wk.s.tiles;    // unit behind the row
@@ -682,8 +694,7 @@ __device__ __forceinline__ void score_role(Smem<kFp4, R>& sm, const Params& P, W
                 P.meta[blockIdx.x] = make_int4(static_cast<int>(row), static_cast<int>(row >> 32), static_cast<int>(e), 0);
             }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.segfull[sb]);
+        bar_arrive(kBarSeg, kScoreThreads + kValueThreads);
     }
 }
 
@@ -713,13 +724,13 @@ __device__ __forceinline__ void value_role(Smem<kFp4, R>& sm, const Params& P, W
         step = 2048;
     }
     float o[R][8][4];
-    int T = 0, seg = 0;
-    for (; wk.left > 0; wk.next(P), ++seg) {
+    int T = 0;
+    for (; wk.left > 0; wk.next(P)) {
         for (int t = 0; t < wk.len; ++t, ++T) {
             const int buf = T & 1, st = T % kS;
-            bool ok = wait(&sm.pfull[buf], (T >> 1) & 1, fail);
-            if (!kFp4) ok = ok && wait(&sm.full[st], (T / kS) & 1, fail);   // complete: makes the copy visible here
-            ok = __all_sync(0xffffffffu, ok);
+            bar_sync(kBarP + buf, kHandover);
+            if (!kFp4) (void)wait<false>(&sm.full[st], (T / kS) & 1, fail);   // complete by now: makes the copy visible here
+            const bool ok = __all_sync(0xffffffffu, !*fail);
             const int resc = sm.resc[buf];
             if (resc == 2) {
 #pragma unroll
@@ -785,21 +796,18 @@ __device__ __forceinline__ void value_role(Smem<kFp4, R>& sm, const Params& P, W
                     }
                 }
             }
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&sm.pempty[buf]);
-                mbar_arrive(kFp4 ? &sm.imgempty[T % kI] : &sm.empty[st]);
-            }
+            bar_arrive(kBarPFree + buf, kHandover);
+            if (kFp4) bar_arrive(kBarImg + T % kI, kHandover);
+            else if (lane == 0) mbar_arrive(&sm.empty[st]);
         }
         // ---- the segment's result ------------------------------------------------------------------
-        const int sb = seg & 1;
-        const bool ok = __all_sync(0xffffffffu, wait(&sm.segfull[sb], (seg >> 1) & 1, fail));
+        bar_sync(kBarSeg, kScoreThreads + kValueThreads);
         const bool whole = wk.t == 0 && wk.len == wk.s.tiles;
         const int j = wk.rq / P.row_groups, h0 = 16 * R * (wk.rq % P.row_groups) + g;
         const int64_t head = ((int64_t)wk.b * P.Q + j) * P.heads + h0;
         const int64_t slot = 2 * (int64_t)blockIdx.x + (wk.t == 0 ? 1 : 0);
-        const float gi = rope ? 1.f : sm.ginv[sb];
-        if (ok) {
+        const float gi = rope ? 1.f : sm.ginv;
+        if (__all_sync(0xffffffffu, !*fail)) {
 #pragma unroll
             for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -807,8 +815,8 @@ __device__ __forceinline__ void value_role(Smem<kFp4, R>& sm, const Params& P, W
                     const int h = 16 * r + 8 * k;   // from this lane's first head
                     float L = 0.f;
 #pragma unroll
-                    for (int i = 0; i < kScoreWarps; ++i) L += sm.lsum[sb][i][r][g + 8 * k];
-                    const float M = sm.mseg[sb][r][g + 8 * k], f = whole ? (L == 0.f ? 0.f : gi / L) : gi;
+                    for (int i = 0; i < kScoreWarps; ++i) L += sm.lsum[i][r][g + 8 * k];
+                    const float M = sm.mseg[r][g + 8 * k], f = whole ? (L == 0.f ? 0.f : gi / L) : gi;
 #pragma unroll
                     for (int q = 0; q < 8; ++q) {
                         const int d = 64 * w + 8 * q + 2 * c;
@@ -823,8 +831,7 @@ __device__ __forceinline__ void value_role(Smem<kFp4, R>& sm, const Params& P, W
                     }
                 }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.segempty[sb]);
+        bar_arrive(kBarSegFree, kScoreThreads + kValueThreads);
     }
 }
 
@@ -861,7 +868,7 @@ __device__ __forceinline__ void copy_role(Smem<kFp4, R>& sm, const Params& P, Wa
             for (int t = 0; t < n_t; ++t, ++T) {
                 const int st = T % kS;
                 bool ok = !*fail;
-                if (T >= kS) ok = ok && wait(&sm.empty[st], (T / kS - 1) & 1, fail);
+                if (T >= kS) ok = ok && wait<true>(&sm.empty[st], (T / kS - 1) & 1, fail);
                 if (!__all_sync(0xffffffffu, ok)) return;
                 // fp4: lane i < 4 copies chunk i; fp8: lane 5 i + k column block k of chunk i (a box of 16 rows by 128 bytes)
                 const int ck = kFp4 ? lane : lane / 5, blk = lane % 5, from = kTileChunks * t + min(ck, kTileChunks - 1);
@@ -901,14 +908,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
         for (int s = 0; s < kS; ++s) {
             mbar_init(&sm.full[s], 1);
             mbar_init(&sm.empty[s], kFp4 ? kGroupWarps : kValueWarps);
-        }
-        for (int s = 0; s < S::kImgs; ++s) mbar_init(&sm.imgempty[s], kValueWarps);
-        for (int s = 0; s < 2; ++s) {
-            mbar_init(&sm.pfull[s], kGroupWarps);
-            mbar_init(&sm.pempty[s], kValueWarps);
-            mbar_init(&sm.marked[s], 1);
-            mbar_init(&sm.segfull[s], kScoreWarps);
-            mbar_init(&sm.segempty[s], kValueWarps);
         }
         sm.fail = 0;
         sm.n_issued = 0;
