@@ -151,6 +151,25 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, i
         "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
         :: "r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar)) : "memory");
 }
+// Shared memory by 32-bit address.
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ int lds8(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
+    return static_cast<int>(v);
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ void sts64(uint32_t a, uint32_t x, uint32_t y) {
+    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(a), "r"(x), "r"(y) : "memory");
+}
 template <bool kZero>   // kZero: d is overwritten
 __device__ __forceinline__ void mma_bf16_frag(float (&d)[4], const uint4& a, uint32_t b0, uint32_t b1) {
     if constexpr (kZero)
@@ -375,8 +394,15 @@ __device__ __forceinline__ void score_fp4(Smem<true, R>& sm, const uint8_t* ch, 
         dx[nt] = see ? kTabDx : 0u;
         dy[nt] = see ? kTabDy : 0u;
     }
-    // words, exponents and fragments come two steps at a time, the words a round ahead of their use (a load may not pass a
-    // store to the image, as far as the compiler knows)
+    // words, exponents and fragments come two steps at a time, the words a round ahead of their use
+    const uint32_t cw = smem_u32(ch) + g * 16 + 4 * c, ce = smem_u32(ch) + kChunk4Exp + g, qa = smem_u32(&sm.qf[0][0][lane]), im = smem_u32(img);
+    uint32_t to[2][4], th[2];
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) to[nt][i] = im + wide[nt] + x[i];
+        th[nt] = im + half[nt] + xh;
+    }
     uint32_t wd[2][2][2];
     int ex[2][2][2];
     auto fetch = [&](int rd) {
@@ -385,8 +411,8 @@ __device__ __forceinline__ void score_fp4(Smem<true, R>& sm, const uint8_t* ch, 
 #pragma unroll
             for (int nt = 0; nt < 2; ++nt) {
                 const int s = 2 * rd + i;
-                wd[rd & 1][i][nt] = *reinterpret_cast<const uint32_t*>(ch + s * 256 + (8 * nt + g) * 16 + 4 * c);
-                ex[rd & 1][i][nt] = ch[kChunk4Exp + s * kChunk + 8 * nt + g];
+                wd[rd & 1][i][nt] = lds32(cw + s * 256 + 128 * nt);
+                ex[rd & 1][i][nt] = lds8(ce + s * kChunk + 8 * nt);
             }
     };
     fetch(0);
@@ -396,7 +422,7 @@ __device__ __forceinline__ void score_fp4(Smem<true, R>& sm, const uint8_t* ch, 
 #pragma unroll
         for (int r = 0; r < R; ++r)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) a[r][k] = sm.qf[r][4 * rd + k][lane];
+            for (int k = 0; k < 4; ++k) a[r][k] = lds128(qa + (r * kQSteps + 4 * rd + k) * 512);
         if (rd + 1 < kSteps / 2) fetch(rd + 1);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
@@ -407,8 +433,7 @@ __device__ __forceinline__ void score_fp4(Smem<true, R>& sm, const uint8_t* ch, 
                 if (kFar && dx[nt] && (j < 0 || j > kMaxJ)) tab.x = tab.y = j < 0 ? 0x7F7F7F7Fu : 0u;
                 uint32_t b0, b1;
                 decode8(wd[rd & 1][i][nt], tab, b0, b1);
-                *reinterpret_cast<uint2*>(img + (s < 12 ? (s >> 2) * kBlkBytes + wide[nt] + x[s & 3] : half[nt] + (xh ^ ((s & 1) << 5)))) =
-                    make_uint2(b0, b1);
+                sts64(s < 12 ? to[nt][s & 3] + (s >> 2) * kBlkBytes : th[nt] ^ ((s & 1) << 5), b0, b1);
                 const uint32_t f0 = bytes_to_f16x2<true, 0>(b0), f1 = bytes_to_f16x2<true, 1>(b0);
                 const uint32_t f2 = bytes_to_f16x2<true, 0>(b1), f3 = bytes_to_f16x2<true, 1>(b1);
 #pragma unroll
@@ -723,6 +748,9 @@ __device__ __forceinline__ void value_role(Smem<kFp4, R>& sm, const Params& P, W
         swz = swz_rope<kFp4>(e);
         step = 2048;
     }
+    uint32_t at[4];   // by q
+#pragma unroll
+    for (int q = 0; q < 4; ++q) at[q] = off + (((col + (rope ? 2 : 1) * q) ^ swz) << 4);
     float o[R][8][4];
     int T = 0;
     for (; wk.left > 0; wk.next(P)) {
@@ -754,7 +782,7 @@ __device__ __forceinline__ void value_role(Smem<kFp4, R>& sm, const Params& P, W
                 }
             }
             if (ok) {
-                const uint32_t base = smem_u32(kFp4 ? sm.img[T % kI] : sm.stage[st]) + off;
+                const uint32_t tile = smem_u32(kFp4 ? sm.img[T % kI] : sm.stage[st]);
                 if (!rope) {
 #pragma unroll
                     for (int kb = 0; kb < kTile / 32; ++kb) {
@@ -766,7 +794,7 @@ __device__ __forceinline__ void value_role(Smem<kFp4, R>& sm, const Params& P, W
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             uint32_t v[4];   // dims 16 q + lane / 4 (+ 8: odd), chunk 2 kb (+ 1: v[2], v[3])
-                            ldmatrix_b8_trans_x2(v, base + kb * step + (((col + q) ^ swz) << 4));
+                            ldmatrix_b8_trans_x2(v, tile + at[q] + kb * step);
 #pragma unroll
                             for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -786,7 +814,7 @@ __device__ __forceinline__ void value_role(Smem<kFp4, R>& sm, const Params& P, W
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             uint32_t v[4];
-                            ldmatrix_b16_trans_x4(v, base + k * step + (((col + 2 * q) ^ swz) << 4));
+                            ldmatrix_b16_trans_x4(v, tile + at[q] + k * step);
 #pragma unroll
                             for (int r = 0; r < R; ++r) {
                                 mma_bf16_frag<false>(o[r][2 * q], a[r], v[0], v[1]);
