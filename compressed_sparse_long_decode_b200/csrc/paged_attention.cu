@@ -84,7 +84,7 @@ constexpr int kHandover = kGroupThreads + kValueThreads;
 
 template <bool kFp4, int R>
 struct Smem {
-    static constexpr int kStages = 4;
+    static constexpr int kStages = !kFp4 && R == 1 ? 5 : 4;
     static constexpr int kStageBytes = kFp4 ? kTileChunks * kChunk4Bytes : kTile8Bytes;
     static constexpr int kImgs = kFp4 ? (R == 1 ? 3 : 2) : 1;   // what fits beside the stages
     uint8_t stage[kStages][kStageBytes];         // tiles as copied (fp8: multiples of 1024 bytes, for the tensor map's swizzle)
@@ -118,6 +118,11 @@ struct Params {
     float scale;
     int heads, rows_per_seq, row_groups, Q, W, sinks;   // row_groups: rows per query
     bool out_bf16, whole;   // whole: shares are whole rows
+};
+
+// fp8: the pages as rows of 576 bytes, by boxes of 128 bytes by 16, 32 and 64 rows.
+struct PageMaps {
+    CUtensorMap rows[3];
 };
 
 // Bounded wait for a copy or a ring slot: false once any such wait of the CTA has given up (this one after about a
@@ -865,7 +870,7 @@ __device__ __forceinline__ void value_role(Smem<kFp4, R>& sm, const Params& P, W
 
 // ---- copy warp -------------------------------------------------------------------------------------
 template <bool kFp4, int R>
-__device__ __forceinline__ void copy_role(Smem<kFp4, R>& sm, const Params& P, Walk wk, int lane, const CUtensorMap* pages_map) {
+__device__ __forceinline__ void copy_role(Smem<kFp4, R>& sm, const Params& P, Walk wk, int lane, const PageMaps& maps) {
     constexpr int kS = Smem<kFp4, R>::kStages;
     volatile int32_t* fail = &sm.fail;
     int T = 0;
@@ -902,6 +907,17 @@ __device__ __forceinline__ void copy_role(Smem<kFp4, R>& sm, const Params& P, Wa
                 const int ck = kFp4 ? lane : lane / 5, blk = lane % 5, from = kTileChunks * t + min(ck, kTileChunks - 1);
                 const int tok = __shfl_sync(0xffffffffu, tok_v, from), row = __shfl_sync(0xffffffffu, row_v, from);
                 const bool mine = ck < kTileChunks && tok >= 0;
+                // fp8: chunks whose rows follow one another go in one request, made by the first of them, all four or in pairs (a
+                // request costs this warp about 110 cycles; 20 boxes a tile held 8 x 64K tokens at 88 us, five give 85)
+                int span = 1;
+                if constexpr (!kFp4) {
+                    const int i = min(ck, kTileChunks - 1), at = kTileChunks * t;
+                    const int tok_p = __shfl_sync(0xffffffffu, tok_v, at + (i ^ 1)), row_p = __shfl_sync(0xffffffffu, row_v, at + (i ^ 1));
+                    const int row_q = __shfl_sync(0xffffffffu, row_v, at + (i ^ 2));
+                    const bool pair = tok >= 0 && tok_p >= 0 && row_p - row == (i & 1 ? -kChunk : kChunk);
+                    const bool quad = __all_sync(0xffffffffu, pair && row_q - row == (i & 2 ? -2 * kChunk : 2 * kChunk));
+                    span = quad ? 4 : pair ? 2 : 1;
+                }
                 if (ck < kTileChunks && (kFp4 || blk == 0)) sm.chunk_tok[st][ck] = tok;
                 const int n = __popc(__ballot_sync(0xffffffffu, mine));
                 if (lane == 0) {
@@ -912,8 +928,9 @@ __device__ __forceinline__ void copy_role(Smem<kFp4, R>& sm, const Params& P, Wa
                 if (mine) {
                     if constexpr (kFp4)
                         bulk_g2s(sm.stage[st] + ck * kChunk4Bytes, P.c.pages + (int64_t)row * kEntry4, kChunk4Bytes, &sm.full[st]);
-                    else
-                        tma_load_2d(sm.stage[st] + blk * kBlkBytes + ck * kChunk * 128, pages_map, blk < 4 ? 128 * blk : kNope, row, &sm.full[st]);
+                    else if ((ck & (span - 1)) == 0)
+                        tma_load_2d(sm.stage[st] + blk * kBlkBytes + ck * kChunk * 128, &maps.rows[span >> 1], blk < 4 ? 128 * blk : kNope, row,
+                                    &sm.full[st]);
                 }
             }
         }
@@ -923,7 +940,7 @@ __device__ __forceinline__ void copy_role(Smem<kFp4, R>& sm, const Params& P, Wa
 }  // namespace
 
 template <bool kFp4, int R>
-__global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __grid_constant__ CUtensorMap pages_map,
+__global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __grid_constant__ PageMaps maps,
                                                                       const __grid_constant__ Params P) {
     using S = Smem<kFp4, R>;
     constexpr int kS = Smem<kFp4, R>::kStages;
@@ -941,7 +958,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
         sm.n_issued = 0;
         fence_barrier_init();
     }
-    if (!kFp4 && warp == kCopyWarp && lane == 0) tma_prefetch_map(&pages_map);
+    if (!kFp4 && warp == kCopyWarp && lane < 3) tma_prefetch_map(&maps.rows[lane]);
     pdl_wait();
     pdl_trigger();
 
@@ -1018,7 +1035,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
             value_role<kFp4, R>(sm, P, wk, warp - kValueWarp, lane);
         } else {
             regs_dec<kRegsCopy<R>>();
-            if (warp == kCopyWarp) copy_role<kFp4, R>(sm, P, wk, lane, &pages_map);
+            if (warp == kCopyWarp) copy_role<kFp4, R>(sm, P, wk, lane, maps);
         }
     }
     __syncthreads();
@@ -1123,10 +1140,10 @@ constexpr int kMergeTiles = 4;   // what cutting rows costs, in tiles of a CTA's
 constexpr size_t kPartBytes = 2 * kMaxR * kHeads * (kDim * sizeof(float) + sizeof(float2)) + sizeof(int4);   // per CTA
 
 template <bool kFp4, int R>
-cudaError_t launch_rows(const CUtensorMap& map, const Params& P, int n_cta, cudaStream_t stream) {
+cudaError_t launch_rows(const PageMaps& maps, const Params& P, int n_cta, cudaStream_t stream) {
     cudaError_t e = set_smem_once(paged_attention_kernel<kFp4, R>, sizeof(Smem<kFp4, R>));
     if (e != cudaSuccess) return e;
-    return launch_pdl(paged_attention_kernel<kFp4, R>, dim3(n_cta), dim3(kThreads), sizeof(Smem<kFp4, R>), stream, map, P);
+    return launch_pdl(paged_attention_kernel<kFp4, R>, dim3(n_cta), dim3(kThreads), sizeof(Smem<kFp4, R>), stream, maps, P);
 }
 }  // namespace
 
@@ -1153,19 +1170,20 @@ cudaError_t launch_paged_attention(const PagedView& c, bool fp4, const uint16_t*
     P.W = W;
     P.sinks = sinks;
     P.out_bf16 = out_bf16;
-    CUtensorMap map = {};   // fp8: the pages as rows of 576 bytes
-    if (!fp4 && !make_tensor_map_2d_u8(&map, c.pages, kEntry, (uint64_t)c.n_pages * c.page_size, 128, kChunk))
-        return cudaErrorInvalidValue;
+    PageMaps maps = {};
+    for (int i = 0; !fp4 && i < 3; ++i)
+        if (!make_tensor_map_2d_u8(&maps.rows[i], c.pages, kEntry, (uint64_t)c.n_pages * c.page_size, 128, kChunk << i))
+            return cudaErrorInvalidValue;
     // Whole rows or cut ones.  The longest row has t tiles, as far as the host knows (the window, or the capacity).
     const int64_t rows = (int64_t)c.batch * P.rows_per_seq;
     int64_t chunks = (c.capacity() + kChunk - 1) / kChunk;
     if (W > 0) chunks = min64(chunks, (min64(sinks, c.capacity()) + kChunk - 1) / kChunk + (min64(W, c.capacity()) + Q - 1 + 2 * kChunk - 2) / kChunk);
     const int64_t t = (chunks + kTileChunks - 1) / kTileChunks, n_cta = min64(num_sms, rows);
     P.whole = (rows + n_cta - 1) / n_cta * t <= rows * t / num_sms + kMergeTiles;
-    cudaError_t e = fp4 ? (R == 2 ? launch_rows<true, 2>(map, P, P.whole ? n_cta : num_sms, stream)
-                                  : launch_rows<true, 1>(map, P, P.whole ? n_cta : num_sms, stream))
-                        : (R == 2 ? launch_rows<false, 2>(map, P, P.whole ? n_cta : num_sms, stream)
-                                  : launch_rows<false, 1>(map, P, P.whole ? n_cta : num_sms, stream));
+    cudaError_t e = fp4 ? (R == 2 ? launch_rows<true, 2>(maps, P, P.whole ? n_cta : num_sms, stream)
+                                  : launch_rows<true, 1>(maps, P, P.whole ? n_cta : num_sms, stream))
+                        : (R == 2 ? launch_rows<false, 2>(maps, P, P.whole ? n_cta : num_sms, stream)
+                                  : launch_rows<false, 1>(maps, P, P.whole ? n_cta : num_sms, stream));
     if (e != cudaSuccess) return e;
     if (P.whole) return cudaGetLastError();
     const int64_t most = rows < num_sms - 1 ? rows : num_sms - 1;
