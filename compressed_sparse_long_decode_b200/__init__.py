@@ -570,13 +570,22 @@ class PagedCache:
         return torch._C._cuda_getCurrentRawStream(self._index)
 
     @classmethod
-    def allocate(cls, batch, context, page_size=64, fmt="fp8", device="cuda"):
-        """An empty cache with room for `context` tokens of each sequence, its pages dealt out in order."""
-        per = -(-context // page_size)
+    def allocate(cls, batch, context, page_size=64, fmt="fp8", device="cuda", window=None, sinks=0, new_tokens=8):
+        """An empty cache with room for `context` tokens of each sequence, its pages dealt out in order.
+        window: for paged_window_attention alone, with that window and `sinks` first tokens and at most
+        new_tokens appended or attended at a time: behind the first tokens' pages the same few pages
+        take turns, so a sequence holds window + sinks tokens (and a page or two) whatever the context."""
+        per = max(1, -(-context // page_size))
         dev = torch.device(device)
         entry = cls.FORMATS[fmt][1] if fmt in cls.FORMATS else 0
-        return cls(torch.zeros((batch * per, page_size * entry), dtype=torch.uint8, device=dev),
-                   torch.arange(batch * per, dtype=torch.int32, device=dev).view(batch, per),
+        held = torch.arange(per, dtype=torch.int32, device=dev)
+        if window is not None:
+            first = -(-sinks // page_size)
+            ring = (window + 2 * new_tokens + page_size - 3) // page_size + 1   # pages that so many tokens in a row may touch
+            held = torch.where(held < first, held, first + (held - first) % ring)
+        n = int(held.max()) + 1
+        table = held[None, :] + n * torch.arange(batch, dtype=torch.int32, device=dev)[:, None]
+        return cls(torch.zeros((batch * n, page_size * entry), dtype=torch.uint8, device=dev), table.contiguous(),
                    torch.zeros(batch, dtype=torch.int32, device=dev), page_size, fmt)
 
 
@@ -698,31 +707,50 @@ class DecodeStack:
     """The attention layers of a hybrid stack for B sequences, each with its own cache (a
     LayerCache per layer), and one decode step through all of them: per layer kv_cache_append,
     then on CSA layers indexer_topk followed by sparse hybrid_decode_attention, on HCA layers
-    dense hybrid_decode_attention.  The layers run in order on the current stream; every
-    call is one of the C-ABI entry points above (this class only holds tensors).
+    dense hybrid_decode_attention; on window layers (raw tokens only, a PagedCache per layer:
+    the window-only blocks beside the hybrid ones) kv_cache_append_paged, then
+    paged_window_attention over the window and the first `sinks` tokens.  The layers run in order
+    on the current stream; every call is one of the C-ABI entry points above (this class only
+    holds tensors).
 
-    kinds: list of "csa" / "hca"; csa_cap / hca_cap: compressed-entry capacity per sequence;
+    kinds: list of "csa" / "hca" / "window" (then: paged_context, the tokens a sequence may reach, and
+    sinks, paged_fmt "fp8" or "fp4", rope_base as for kv_cache_append_paged); csa_cap / hca_cap: compressed-entry capacity per sequence;
     pos_bias4 [4], pos_bias128 [128], w_idx [512,64]: the pooling biases and the indexer
     projection (shared by the layers of a kind here; per-layer weights only change bytes)."""
 
     def __init__(self, batch, kinds, csa_cap, hca_cap, window, topk, pos_bias4, pos_bias128, w_idx,
-                 device="cuda"):
+                 device="cuda", sinks=0, paged_context=None, paged_fmt="fp8", rope_base=0.0):
         self.batch, self.kinds, self.window, self.topk = batch, list(kinds), window, topk
+        self.sinks, self.rope_base = sinks, rope_base
         dev = torch.device(device)
-        self.layers = [LayerCache(batch, csa_cap, 4, window, pos_bias4, w_idx, device=dev) if k == "csa"
-                       else LayerCache(batch, hca_cap, 128, window, pos_bias128, device=dev) for k in self.kinds]
-        csa = [c for c in self.layers if c.ratio == 4]
-        caps = [c.capacity for c in self.layers]
+
+        def layer(kind):
+            if kind == "window":
+                if paged_context is None:
+                    raise CsldError('paged_context is required with "window" layers')
+                return PagedCache.allocate(batch, paged_context, fmt=paged_fmt, device=dev, window=window, sinks=sinks)
+            return (LayerCache(batch, csa_cap, 4, window, pos_bias4, w_idx, device=dev) if kind == "csa"
+                    else LayerCache(batch, hca_cap, 128, window, pos_bias128, device=dev))
+
+        self.layers = [layer(k) for k in self.kinds]
+        hybrid = [c for c in self.layers if isinstance(c, LayerCache)]
+        csa = [c for c in hybrid if c.ratio == 4]
         self.ws_idx = indexer_workspace(batch, csa[0].capacity, topk, dev) if csa else None
-        self.ws_att = attention_workspace(batch, max(caps), topk, window, dev)
+        self.ws_att = attention_workspace(batch, max(c.capacity for c in hybrid), topk, window, dev) if hybrid else None
+        self.ws_paged = paged_attention_workspace(dev) if len(hybrid) < len(self.layers) else None
         self.sel = torch.empty((batch, topk), dtype=torch.int32, device=dev)
         self.err = torch.zeros(1, dtype=torch.int32, device=dev)
 
     def kv_bytes_per_sequence(self, context):
         """Bytes one sequence's cache holds at `context` raw tokens: compressed entries (576 B),
-        indexer keys (32 B codes + 8 B scales) on CSA layers, the window ring and the tail."""
+        indexer keys (32 B codes + 8 B scales) on CSA layers, the window ring and the tail; the pages of
+        window layers."""
         total = 0
         for c in self.layers:
+            if isinstance(c, PagedCache):   # the pages that its tokens lie in
+                pages = c.page_table[0, :-(-context // c.page_size)]
+                total += int(pages.unique().numel()) * c.page_size * c.entry_bytes
+                continue
             n = context // c.ratio
             total += n * ENTRY_BYTES + (n * (IKEY_BYTES + 8) if c.has_indexer else 0)
             total += min(self.window, context) * ENTRY_BYTES + (context % c.ratio) * (2 * DIM + 4)
@@ -733,8 +761,13 @@ class DecodeStack:
         [L,B] f32, q [L,B,16,512] bf16, q_idx [L,B,4,64] f32, head_w [L,B,4] f32; out
         [L,B,16,512] f32, lse [L,B,16] f32 or None (device tensors)."""
         for i, c in enumerate(self.layers):
-            kv_cache_append(c, kv_new[i], gate_new[i], self.err)
             l_i = None if lse is None else lse[i]
+            if isinstance(c, PagedCache):
+                kv_cache_append_paged(c, kv_new[i].unsqueeze(1), rope_base=self.rope_base, err=self.err)
+                paged_window_attention(c, q[i].unsqueeze(1), self.window, self.sinks, scale, out=out[i].unsqueeze(1),
+                                       lse=None if l_i is None else l_i.unsqueeze(1), ws=self.ws_paged, err=self.err)
+                continue
+            kv_cache_append(c, kv_new[i], gate_new[i], self.err)
             if c.has_indexer:
                 indexer_topk(c.ikeys, c.iscales, c.seq_len, 4, q_idx[i], head_w[i], self.topk, out=self.sel,
                              ws=self.ws_idx, err=self.err)

@@ -319,6 +319,127 @@ def test_decode_run_append_window_and_full_together(csld, fmt):
     assert c.dev.err.item() == 0
 
 
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+def test_decode_stack_with_window_layers(csld, fmt):
+    """A stack of a CSA, an HCA and two window layers over 150 steps: the window layers keep a window of 32
+    and 5 first tokens in a ring of pages that is smaller than the context, and match the reference
+    over the tokens that they were given; the hybrid layers give what a stack without window layers gives."""
+    B, steps, W, S, L = 2, 150, 32, 5, 4
+    inp = synth.prefill_inputs(8, seed=0)
+    make = lambda kinds: csld.DecodeStack(B, kinds, 64, 8, W, 16, inp["bias4"], inp["bias128"], inp["w_idx"],   # noqa: E731
+                                          sinks=S, paged_context=200, paged_fmt=fmt, rope_base=BASE)
+    kinds = ["window", "csa", "hca", "window"]
+    stack, plain = make(kinds), make(["csa", "hca"])
+    assert stack.layers[0].pages.shape[0] < B * stack.layers[0].max_pages
+    assert stack.kv_bytes_per_sequence(steps) > plain.kv_bytes_per_sequence(steps)
+    g = synth.gen(13)
+    refs = []
+    for _ in range(2):
+        per = 4
+        pages = np.zeros((B * per, 64 * R.ENTRY[fmt]), np.uint8)
+        refs.append(R.Cache(pages, np.arange(B * per, dtype=np.int32).reshape(B, per), np.zeros(B, np.int32), 64, fmt))
+    for s in range(steps):
+        x = _tokens(g, L, B)
+        gate = torch.randn(L, B, generator=g)
+        q = torch.randn(L, B, 16, 512, generator=g).to(torch.bfloat16)
+        qi, hw = torch.randn(L, B, 4, 64, generator=g), torch.randn(L, B, 4, generator=g).abs()
+        a = [t.cuda() for t in (x, gate, q, qi, hw)]
+        out, lse = torch.zeros(L, B, 16, 512, device="cuda"), torch.zeros(L, B, 16, device="cuda")
+        o2, l2 = torch.zeros(2, B, 16, 512, device="cuda"), torch.zeros(2, B, 16, device="cuda")
+        stack.step(*a, SCALE, out, lse)
+        plain.step(*[t[1:3].contiguous() for t in a], SCALE, o2, l2)
+        for k, i in enumerate((0, 3)):
+            refs[k].append(x[i].double().numpy()[:, None], None, None, BASE)
+        if s in (0, 20, 70, 149):
+            torch.cuda.synchronize()
+            assert torch.equal(out[1:3], o2) and torch.equal(lse[1:3], l2)
+            for k, i in enumerate((0, 3)):
+                ref = R.attention(refs[k], q[i].double().numpy()[:, None], SCALE, W, S)
+                # the stored RoPE dims may differ by one bf16 step (2^-7 of the value): on A and on the logits (delta grows
+                # from 512 * 2^-24 to 64 dims' 2^-7, at most)
+                o, l, A, d, F = ref
+                R.assert_attention(out[i][:, None], lse[i][:, None], (o, l, 3 * A, d * 2.0 ** 8, F), f"{fmt} layer {i} step {s}")
+    assert stack.err.item() == 0
+
+
+def test_two_streams_with_their_own_workspaces_and_inputs_of_another_stream(csld):
+    """Two attention calls at once on two streams, each with its workspace, give what they give alone; a
+    sequence of calls on a side stream is ordered by that stream alone."""
+    c = Pair(csld, [3000, 1500, 77], 64, "fp4", seed=31)
+    q = [torch.randn(3, 1, 16, 512, generator=synth.gen(k)).to(torch.bfloat16).cuda() for k in range(2)]
+    want = [[t.clone() for t in csld.paged_decode_attention(c.dev, x, SCALE)] for x in q]
+    streams, ws = [torch.cuda.Stream() for _ in range(2)], [csld.paged_attention_workspace() for _ in range(2)]
+    outs = [(torch.zeros(3, 1, 16, 512, dtype=torch.bfloat16, device="cuda"), torch.zeros(3, 1, 16, device="cuda")) for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for k in range(2):
+            with torch.cuda.stream(streams[k]):
+                csld.paged_decode_attention(c.dev, q[k], SCALE, out=outs[k][0], lse=outs[k][1], ws=ws[k])
+    torch.cuda.synchronize()
+    for k in range(2):
+        assert torch.equal(outs[k][0], want[k][0]) and torch.equal(outs[k][1], want[k][1])
+
+
+def test_results_do_not_depend_on_the_run(csld):
+    """Same call, same bits: no atomics decide an order (long and short rows, cut and whole ones)."""
+    for fmt in ("fp8", "fp4"):
+        c = Pair(csld, [2500, 10, 900], 32, fmt, seed=8)
+        for H in (16, 40):
+            q = torch.randn(3, 2, H, 512, generator=synth.gen(H)).to(torch.bfloat16).cuda()
+            a = [t.clone() for t in csld.paged_decode_attention(c.dev, q, SCALE)]
+            for _ in range(5):
+                b = csld.paged_decode_attention(c.dev, q, SCALE)
+                assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+def test_offsets_past_2_to_the_31_bytes(csld, fmt):
+    """Pages whose bytes begin past 2^31 (and 2^32) in the pool, and many sequences of which most are empty:
+    more than the 640 that one pass of the scan covers."""
+    page, B = 64, 1500
+    entry = R.ENTRY[fmt]
+    n_pages = (2 ** 32 + 2 ** 28) // (page * entry)
+    pool = torch.empty((n_pages, page * entry), dtype=torch.uint8, device="cuda")
+    lens = [0] * B
+    for b, n in ((0, 5), (7, 130), (699, 64), (1203, 200), (1499, 1)):
+        lens[b] = n
+    table = torch.full((B, 4), -1, dtype=torch.int32)
+    at = n_pages
+    for b in range(B):
+        for i in range(-(-lens[b] // page)):
+            at -= 1 if b != 7 else (2 ** 31) // (page * entry) // 2
+            table[b, i] = at
+    seq = torch.tensor(lens, dtype=torch.int32)
+    c = csld.PagedCache(pool, table.cuda(), torch.zeros(B, dtype=torch.int32, device="cuda"), page, fmt)
+    x = _tokens(synth.gen(3), B, 200)
+    csld.kv_cache_append_paged(c, x.cuda(), n_new=seq.cuda())
+    q = torch.randn(B, 1, 16, 512, generator=synth.gen(5)).to(torch.bfloat16)
+    o, l = csld.paged_decode_attention(c, q.cuda(), SCALE)
+    torch.cuda.synchronize()
+    assert c.err.item() == 0 and torch.equal(c.seq_len.cpu(), seq)
+    keep = [b for b in range(B) if lens[b]]
+    small = R.Cache(np.zeros((4 * len(keep), page * entry), np.uint8), np.arange(4 * len(keep), dtype=np.int32).reshape(-1, 4),
+                    np.zeros(len(keep), np.int32), page, fmt)
+    small.append(x[keep].double().numpy(), seq[keep].numpy(), None, 0.0)
+    R.assert_attention(o[keep], l[keep], R.attention(small, q[keep].double().numpy(), SCALE), fmt)
+    none = [b for b in range(B) if not lens[b]]
+    assert (o[none] == 0).all() and torch.isneginf(l[none]).all()
+    del pool, c
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+def test_lengths_out_of_range_are_reported_and_bounded(csld, fmt):
+    c = Pair(csld, [40, 40], 16, fmt, seed=12)
+    q = torch.randn(2, 1, 16, 512, generator=synth.gen(2)).to(torch.bfloat16)
+    c.dev.seq_len.copy_(torch.tensor([-5, 40], dtype=torch.int32))
+    o, l = csld.paged_window_attention(c.dev, q.cuda(), 20, 2, SCALE)
+    torch.cuda.synchronize()
+    assert c.dev.err.item() == 4 and (o[0] == 0).all() and torch.isneginf(l[0]).all()
+    c.ref.seq_len[:] = [0, 40]
+    R.assert_attention(o, l, R.attention(c.ref, q.double().numpy(), SCALE, 20, 2), fmt)
+
+
 def test_binding_refuses_bad_tensors(csld):
     c = csld.PagedCache.allocate(2, 100, 16, "fp4")
     q = torch.zeros(2, 1, 16, 512, dtype=torch.bfloat16, device="cuda")
