@@ -19,29 +19,38 @@
 // Which tensor instructions.  With 16 heads one side of every product is 16 rows.  A tcgen05.mma reads its
 // 128-row operand, here the entries, from shared memory at 128 B a cycle: 45 cycles for 128 x 32 x 32 (measured;
 // 16 at full rate), and a version of this kernel built on it moved 326 KB through shared memory for 96 fp4
-// entries and took 3000 cycles (1M fp4 tokens 222 us).  The warp-level E4M3 mma.sync runs at 3800 MAC a cycle
-// and SM (measured) with its operands in registers: the query stays there for a whole row, 4-bit keys go from a
-// code word to a B fragment without touching shared memory, and only the values take that way.
+// entries (2,550 cycles at best) and took 3,000 (1M fp4 tokens 222 us).  Warp-level E4M3 mma.sync is slower still
+// (62 cycles an m16n8k32 and scheduler: 538 us).  The warp-level f16 one runs at 1,013 MAC a cycle and SM (measured;
+// 16.2 cycles an entry), takes the bf16 query exactly, P in one term, and 4-bit keys in registers: a code word
+// becomes a B fragment without touching shared memory, and only the values take that way.
 //
-// A CTA's roles (16 warps; registers moved from the copy warps to the score warps):
-//   copy   (warp 12)    pages -> a ring of tiles in shared memory: fp4 chunks as they lie (5888 contiguous bytes, bulk
-//                       copies), fp8 entries as five 128-byte column blocks with the 128-byte swizzle (tensor map)
-//   score  (warps 0-3)  warp w takes the tile's chunk w.  S = Q K^T by m16n8k32 E4M3 MMAs, the bf16 query as two E4M3
-//                       terms (exact: 4 + 4 significant bits and a sign), the RoPE dims by bf16 MMAs.  fp4: lane
-//                       (n, c) = (lane / 4, lane % 4) decodes word c of entry n's group: its 8 codes are that
-//                       lane's whole share of the group's 32-dim MMA step, in whatever order, since the query's
-//                       dims are laid out the same.  E2M1 -> E4M3 is a byte permute through 8 table bytes, 2^(6-j)
-//                       times the grid, j = the entry's largest exponent minus the group's: all normal numbers, so
-//                       j only subtracts 8 j from each (j > 11 or a NaN group: from a table in shared memory); an
-//                       entry's decoded bytes are its values over one power of two f_e, applied to S and to P.
-//                       The decoded bytes also go to the value image.  Then the softmax: p relative to a mark nm that
-//                       is only raised when some p exceeds 2^10..15, one meeting of the four warps a tile, and P as
-//                       A fragments in shared memory: p f_e as three E5M2 terms, p as bf16 for the RoPE dims.
-//   value  (warps 4-11) warp w owns 64 of the 512 dims and keeps its O in registers: O += P V by m16n8k32 E5M2 x E4M3
-//                       MMAs, V fragments by transposing 8-bit matrix loads of the image (fp8: of the copied tile
-//                       itself); warp 11 the RoPE dims, bf16
-// Rows of masked or missing tokens are zeroed before they are used, whatever was in them.  Every wait is
-// bounded; a wait that gives up sets CSLD_DEVERR_TIMEOUT and all roles run out without waiting.
+// A CTA's roles (20 warps; registers are moved from the copy warps to the others):
+//   copy   (warp 16)    pages -> a ring of 64-entry tiles in shared memory: fp4 chunks as they lie (5,888 contiguous
+//                       bytes, bulk copies), fp8 entries as five 128-byte column blocks with the 128-byte swizzle (tensor maps)
+//   score  (warps 0-7)  two groups of four take the tiles in turn, so that one's softmax runs under the other's
+//                       products; warp w of a group takes the tile's chunk w.  S = Q K^T, the RoPE dims by bf16 MMAs.
+//                       fp4: lane (n, c) = (lane / 4, lane % 4) decodes word c of entry n's group: its 8 codes are the
+//                       lane's whole share of the group's two 16-dim MMA steps, in whatever order, since the query's
+//                       dims are laid out the same.  E2M1 -> E5M2 is a byte permute through 8 table bytes, 2^(13-j)
+//                       times the grid, j = the entry's largest exponent minus the group's: all normal numbers, so j
+//                       only subtracts 4 j from each (a group 2^-26 or less of the entry's largest is zero); E5M2 is
+//                       f16's upper byte, so another permute makes the f16 pair.  An entry's decoded bytes are its values
+//                       over one power of two f_e, applied to S and to P.  They also go to the value image.  fp8: the
+//                       hardware's E4M3 -> f16 converts.  Then the softmax: p relative to a mark nm that is raised only
+//                       when some p exceeds it by 2^10, the marks handed from tile to tile, one meeting of the
+//                       four warps a tile, and P as A fragments in shared memory: p f_e g in f16 (2^-11), for the RoPE
+//                       dims p in bf16.
+//   value  (warps 8-15) warp w owns 64 of the 512 dims and keeps its O in registers: O += P V, V fragments by
+//                       transposing 8-bit matrix loads of the image (fp8: of the copied tile itself); the last warp the
+//                       RoPE dims, bf16
+// Where a query has more than 16 heads a row is two groups of 16 (R = 2): keys are decoded and values loaded once for both.
+//
+// What bounds it (fp4, R = 1, a 64-entry tile, 1M tokens; cycles an SM): HBM 975; f16 MMAs 1,024; ALU (permutes, masks) 1,040;
+// shared memory about 1,700 wavefronts; 6,500 instructions, 1,630 a scheduler; taken: 2,630, 0.6 instructions a cycle
+// and scheduler.  176 us, 2.2 TB/s, 0.34 of the copy rate.  fp8: 86 us for 8 x 64K tokens, 3.5 TB/s, 0.53.
+// A third score group (with four value warps of 128 dims) gave 181 us, more or larger stages nothing.
+// Rows of masked or missing tokens are zeroed before they are used, whatever was in them.  The waits for copies are
+// bounded; one that gives up sets CSLD_DEVERR_TIMEOUT and all roles run out without waiting for copies.
 #include <stdint.h>
 
 #include "kernels.cuh"
@@ -77,7 +86,9 @@ template <bool kFp4> constexpr float kOver = kFp4 ? 10.f : 15.f;
 constexpr float kFeSet = 8.f, kFeMost = 32.f, kUnset = 1e30f;
 // hardware barriers: the score groups' own (1, 2), both groups' (3); from a group to the value warps: P of a tile is there
 // (4, 5), back: its slot is free (6, 7), a value image is free (8, 9, 10); from group to group: the marks are there (11,
-// 12); from the score to the value warps: a segment's sums (13), back: taken (14)
+// 12); from the score to the value warps: a segment's sums (13), back: taken (14).  No warp can meet an earlier or a
+// later use of a barrier than its own: P slots and marks keep to one group each (a group's tiles have one parity); the
+// images turn among three, so that their groups alternate, but the marks of the tile between order the turns.
 constexpr int kBarGroup = 1, kBarScore = 3, kBarP = 4, kBarPFree = 6, kBarImg = 8, kBarMark = 11, kBarSeg = 13, kBarSegFree = 14;
 constexpr int kGroupThreads = 32 * kGroupWarps, kScoreThreads = 32 * kScoreWarps, kValueThreads = 32 * kValueWarps;
 constexpr int kHandover = kGroupThreads + kValueThreads;
@@ -97,7 +108,7 @@ struct Smem {
     float nm[R][kHeads], gs;                     // the marks
     float tmax[2][kGroupWarps][R][kHeads], femax[2][kGroupWarps];
     float lsum[kScoreWarps][R][kHeads], mseg[R][kHeads], ginv;   // a segment's sums, marks and 1 / g
-    int32_t chunk_tok[kStages][kTileChunks];           // first token of a tile's chunks; -1: none
+    int32_t chunk_tok[kStages][kTileChunks];     // first token of a tile's chunks; -1: none
     int32_t resc[2];                             // 0: O stays, 1: O *= f, 2: O = 0 (first tile of a segment)
     uint64_t full[kStages], empty[kStages];
     int64_t red[kThreads / 32], prefix;
@@ -111,8 +122,8 @@ struct Params {
     const uint16_t* q;
     void* out;
     float* lse;
-    float* opart;        // [2 CTAs][16][512]
-    float2* mlpart;      // [2 CTAs][16]
+    float* opart;        // [2 CTAs][a row's heads][512]
+    float2* mlpart;      // [2 CTAs][a row's heads]
     int4* meta;          // [CTAs]: (row low, row high, last CTA, -) of the cut row that begins there; last CTA -1: none
     int32_t* err;
     float scale;

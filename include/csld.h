@@ -456,10 +456,11 @@ CSLD_API csld_status kv_cache_read_paged(const csld_paged_cache* cache, const in
  *   q [batch][Q][heads][512] bf16; out the same shape, fp32 (out_type CSLD_OUT_F32) or bf16
  *   (CSLD_OUT_BF16); lse_out [batch][Q][heads] f32 or NULL; 1 <= heads <= CSLD_PAGED_MAX_HEADS,
  *   1 <= Q <= CSLD_MULTI_MAX_Q, 1 <= W, 0 <= sinks; q, out, ws 16-byte aligned.
- * Products: the bf16 query against the stored codes exactly, softmax weights as two E4M3 terms (about
- * 2^-9) for the 8- and 4-bit dims and as bf16 for the RoPE dims; sums and statistics in fp32.  An fp4
- * entry's group whose scale lies more than 2^14 below the entry's largest is rounded at 2^-9 of ... that
- * span (its values are below 2^-14 of the entry's largest).
+ * Products: the bf16 query against the stored codes exactly (down to 2^-21 of a head's largest value),
+ * softmax weights rounded to f16 (2^-11) for the 8- and 4-bit dims and to bf16 for the RoPE dims; sums and
+ * statistics in fp32.  A group of an fp4 entry whose scale lies more than 2^26 below the entry's largest
+ * counts as zero.  A seq_len below 0 or above max_pages * page_size sets CSLD_DEVERR_SEQ_LEN and counts
+ * as 0 or as that.  The order of every sum is fixed by the shapes and lengths: same call, same bits.
  * Workspace: csld_paged_attention_workspace_size() bytes (the same for every shape), no initial
  * contents needed; calls that share one must not overlap on the GPU. */
 #define CSLD_OUT_F32 0

@@ -1,15 +1,15 @@
 """The paged entry cache and its attentions in numpy, 64 bits, from the format's definition (no code of
 the library): entries are encoded and decoded value by value, attention is a plain softmax.
 
-Bounds on the library's outputs (assert_attention).  The softmax weights p of the stored 8- and 4-bit
-dims are rounded to two E4M3 terms: 2^-4 of 2^-4 = 2^-8 of p, and no finer than half of E4M3's smallest
-step, 2^-10, where the largest weight of 32 tokens (times its fp4 entry's scale) lies in 2^7..2^8: with
-Vmax the largest of an entry's 448 values, each of the 32 errs by at most 2^-17 max(p Vmax) there, and
-a chunk of 16 tokens shares its 32 with one other, so F = 32 * (sum over chunks of max(p Vmax)) bounds
-the sum of these.  (Weights below 2^-126 of the largest vanish: less than that.)  For the RoPE dims p is
-rounded to bf16, 2^-8.  A logit is a 512-term fp32 sum, off by at most delta = 512 * 2^-24 * scale *
-sum|q||k|, the exponential by 2^-22, which move every weight by that relatively, and the denominator
-too.  bf16 outputs add their rounding, 2^-8 of the value.  With A = sum p |v|:
+Bounds on the library's outputs (assert_attention).  A softmax weight p is rounded to 2^-8 of itself at
+most (bf16, the RoPE dims; f16, the others: 2^-11).  Small ones are rounded no finer than an absolute
+step: with Vmax the largest of an entry's 448 values, 2^-17 of the largest p Vmax of 32 tokens is allowed
+to each of them; a chunk of 16 tokens shares its 32 with one other, so F = 32 * (sum over chunks of
+max(p Vmax)) bounds the sum of these.  (f16's step is 2^-24 of the largest p Vmax of all tokens: less than
+that for up to 4096 tokens; weights below 2^-126 of the largest vanish: less than that.)  A logit is a
+512-term fp32 sum, off by at most delta = 512 * 2^-24 * scale * sum|q||k|, the exponential by 2^-22, which
+move every weight by that relatively, and the denominator too.  bf16 outputs add their rounding, 2^-8 of
+the value.  With A = sum p |v|:
     |out - ref| <= (2^-8 + 2 delta + 2^-21) A + 2^-17 F + (2^-8 |ref| for bf16 outputs)
     |lse - ref| <= delta + 2^-20 (1 + |ref|)        (fp32 sums of at most 2^17 terms, in pieces)
 """

@@ -218,9 +218,9 @@ def test_fp4_entries_of_very_unlike_magnitudes(csld):
     c.dev.pages.copy_(torch.from_numpy(c.ref.pages))
     q = torch.randn(1, 1, 16, 512, generator=g).to(torch.bfloat16)
     ref = list(R.attention(c.ref, q.double().numpy(), SCALE))
-    # The kernel holds a group at most 2^14 below its entry's largest scale exactly, others rounded to
-    # 2^-16 of that scale, which is at most 1 here (max|x| < 6): 2^-16 on an output (A enters times
-    # 2^-8), and on a logit scale * 32 dims * max|q| (< 6) * 2^-16 < 2^-12.
+    # A kernel may round a group whose scale lies far below its entry's largest: to 2^-16 of that scale, which
+    # is at most 1 here (max|x| < 6), is allowed: 2^-16 on an output (A enters times 2^-8), and on a logit scale *
+    # 32 dims * max|q| (< 6) * 2^-16 < 2^-12.
     ref[2] = ref[2] + 2.0 ** -8
     ref[3] = ref[3] + 2.0 ** -12
     o, l = csld.paged_decode_attention(c.dev, q.cuda(), SCALE)
