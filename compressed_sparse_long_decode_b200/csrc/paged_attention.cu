@@ -64,9 +64,9 @@ namespace {
 constexpr int kThreads = 640;
 constexpr int kGroupWarps = 4, kScoreWarps = 8, kValueWarp = 8, kValueWarps = 8, kCopyWarp = 16;
 // registers a thread: the launch gives 640 x 96 = 61,440; R = 1 takes 256 x 112 + 256 x 104 + 128 x 40 = 60,416 of
-// them, R = 2 256 x 120 + 256 x 104 + 128 x 32 = 61,440
-template <int R> constexpr int kRegsScore = R == 1 ? 112 : 120;
-constexpr int kRegsValue = 104;
+// them, R = 2 256 x 112 + 256 x 112 + 128 x 32 = 61,440
+constexpr int kRegsScore = 112;
+template <int R> constexpr int kRegsValue = R == 1 ? 104 : 112;
 template <int R> constexpr int kRegsCopy = R == 1 ? 40 : 32;
 constexpr int kTile = 64, kTileChunks = kTile / kChunk;   // entries per tile; a chunk per warp of a score group
 static_assert(kTileChunks == kGroupWarps, "a group's warp w takes chunk w");
@@ -104,7 +104,6 @@ struct Smem {
     uint4 p16[2][R][kTileChunks][32];            // P in f16: [chunk][lane] A fragments
     uint4 pbf[2][R][kTileChunks][32];            // bf16 P
     float fn[2][R][kHeads], fr[2][R][kHeads];    // factors of O before a tile's MMAs (448 dims; RoPE dims)
-    float c2[R][kHeads], sq[R][kHeads];          // logit factors (log2 units), scales of the query
     float nm[R][kHeads], gs;                     // the marks
     float tmax[2][kGroupWarps][R][kHeads], femax[2][kGroupWarps];
     float lsum[kScoreWarps][R][kHeads], mseg[R][kHeads], ginv;   // a segment's sums, marks and 1 / g
@@ -323,64 +322,59 @@ __device__ __forceinline__ void store_out2(const Params& P, int64_t at, float a,
 }
 
 // ---- the query ---------------------------------------------------------------------------------
-// A row's A fragments, by all 256 score threads (warp 0..7): each head scaled by a power of two so that its largest
-// value lies in 2^7..2^8 (exact in f16 down to 2^-21 of it; scale_query finds it).  MMA step k < 28 holds of every 32 dims half
-// (k % 2), lane (g, c) the dims 8c + 4 (k % 2) .. + 3 of heads g and g + 8: the order in which a lane's eight key
-// bytes come; steps 28..31 the RoPE dims 16 (k - 28) + 4c .. + 3 in bf16.
-template <bool kFp4, int R>
-__device__ __forceinline__ void scale_query(Smem<kFp4, R>& sm, const Params& P, int b, int rq, int warp, int lane) {
-    const int j = rq / P.row_groups, hr = 16 * R * (rq % P.row_groups);   // the row's first head
-    const uint16_t* q = P.q + (((int64_t)b * P.Q + j) * P.heads + hr) * kDim;
-    // largest value of head 2 warp + lane / 16, by 16 lanes of 32 dims each
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const int h = 16 * r + 2 * warp + (lane >> 4);
-        uint32_t top = 0;
-        if (hr + h < P.heads) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint4 v = __ldg(reinterpret_cast<const uint4*>(q + h * kDim) + 4 * (lane & 15) + i);
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) top = max(top, max(w[k] & 0x7FFFu, (w[k] >> 16) & 0x7FFFu));
-            }
-        }
-#pragma unroll
-        for (int o = 1; o < 16; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const int sh = top ? max(-100, min(100, 134 - static_cast<int>(top >> 7))) : 0;
-        if ((lane & 15) == 0) {
-            sm.c2[r][2 * warp + (lane >> 4)] = P.scale * 1.4426950408889634f * pow2f(-sh);
-            sm.sq[r][2 * warp + (lane >> 4)] = pow2f(sh);
-        }
+// A row's A fragments, by the eight score warps: each head scaled by a power of two so that its largest value lies in
+// 2^7..2^8 (exact in f16 down to 2^-21 of it).  MMA step k < 28 holds of every 32 dims half (k % 2), lane (g, c) the
+// dims 8c + 4 (k % 2) .. + 3 of heads g and g + 8: the order in which a lane's eight key bytes come; steps 28..31 the
+// RoPE dims 16 (k - 28) + 4c .. + 3 in bf16.  Warp w builds the steps 4w .. 4w + 3.
+template <int R>
+struct QueryPart {
+    static constexpr int kN = kQSteps / kScoreWarps;
+    uint2 v[R][kN][2];   // [step][head g, g + 8]: four dims
+    __device__ __forceinline__ static int dim_of(int k, int c) {
+        return k < 2 * kSteps ? 32 * (k >> 1) + 8 * c + 4 * (k & 1) : kNope + 16 * (k - 2 * kSteps) + 4 * c;
     }
-}
-template <bool kFp4, int R>
-__device__ __forceinline__ void build_fragments(Smem<kFp4, R>& sm, const Params& P, int b, int rq, int warp, int lane) {
-    const int j = rq / P.row_groups, hr = 16 * R * (rq % P.row_groups), g = lane >> 2, c = lane & 3;
-    const uint16_t* q = P.q + (((int64_t)b * P.Q + j) * P.heads + hr) * kDim;
+    __device__ __forceinline__ void load(const Params& P, int b, int rq, int warp, int g, int c) {
+        const int j = rq / P.row_groups, hr = 16 * R * (rq % P.row_groups);   // the row's first head
+        const uint16_t* q = P.q + (((int64_t)b * P.Q + j) * P.heads + hr) * kDim;
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const float s[2] = {sm.sq[r][g], sm.sq[r][g + 8]};
+        for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int i = 0; i < kQSteps / kScoreWarps; ++i) {
-            const int k = warp * (kQSteps / kScoreWarps) + i;
-            const int d = k < 2 * kSteps ? 32 * (k >> 1) + 8 * c + 4 * (k & 1) : kNope + 16 * (k - 2 * kSteps) + 4 * c;
+            for (int i = 0; i < kN; ++i)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int h = 16 * r + g + 8 * u;
+                    v[r][i][u] = hr + h < P.heads ? __ldg(reinterpret_cast<const uint2*>(q + h * kDim + dim_of(warp * kN + i, c)))
+                                                  : make_uint2(0, 0);
+                }
+    }
+    // largest magnitude (bf16 bits) of head g + 8 u of group r in this warp's steps
+    __device__ __forceinline__ uint32_t top(int r, int u) const {
+        uint32_t t = 0;
+#pragma unroll
+        for (int i = 0; i < kN; ++i)
+            t = max(t, max(max(v[r][i][u].x & 0x7FFFu, (v[r][i][u].x >> 16) & 0x7FFFu),
+                           max(v[r][i][u].y & 0x7FFFu, (v[r][i][u].y >> 16) & 0x7FFFu)));
+        t = max(t, __shfl_xor_sync(0xffffffffu, t, 1));
+        return max(t, __shfl_xor_sync(0xffffffffu, t, 2));
+    }
+    template <bool kFp4>
+    __device__ __forceinline__ void store(Smem<kFp4, R>& sm, int r, const float (&sq)[2], int warp, int lane) const {
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+            const int k = warp * kN + i;
             uint32_t a[4];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int h = 16 * r + g + 8 * u;
-                const uint2 v = hr + h < P.heads ? __ldg(reinterpret_cast<const uint2*>(q + h * kDim + d)) : make_uint2(0, 0);
-                const uint32_t w[2] = {v.x, v.y};
+            for (int u = 0; u < 2; ++u)
 #pragma unroll
                 for (int n = 0; n < 2; ++n) {
-                    const float x0 = bf16_bits_to_f32(w[n]) * s[u], x1 = bf16_bits_to_f32(w[n] >> 16) * s[u];
+                    const uint32_t w = n ? v[r][i][u].y : v[r][i][u].x;
+                    const float x0 = bf16_bits_to_f32(w) * sq[u], x1 = bf16_bits_to_f32(w >> 16) * sq[u];
                     a[u + 2 * n] = k < 2 * kSteps ? f32x2_to_f16x2(x0, x1) : f32x2_to_bf16x2_bits(x0, x1);
                 }
-            }
             sm.qf[r][k][lane] = make_uint4(a[0], a[1], a[2], a[3]);
         }
     }
-}
+};
 
 // ---- score warps ---------------------------------------------------------------------------------
 // S of this warp's 16 entries, fp4: decodes them (into the value image too).  kFar: some group lies more than 2^26 below
@@ -410,7 +404,8 @@ __device__ __forceinline__ void score_fp4(Smem<true, R>& sm, const uint8_t* ch, 
         dx[nt] = see ? kTabDx : 0u;
         dy[nt] = see ? kTabDy : 0u;
     }
-    // words, exponents and fragments come two steps at a time, the words a round ahead of their use
+    // words, exponents and fragments come kPer steps at a time (as registers allow), the words a round ahead of their use
+    constexpr int kPer = R == 1 ? 2 : 1;
     const uint32_t cw = smem_u32(ch) + g * 16 + 4 * c, ce = smem_u32(ch) + kChunk4Exp + g, qa = smem_u32(&sm.qf[0][0][lane]), im = smem_u32(img);
     uint32_t to[2][4], th[2];
 #pragma unroll
@@ -419,32 +414,32 @@ __device__ __forceinline__ void score_fp4(Smem<true, R>& sm, const uint8_t* ch, 
         for (int i = 0; i < 4; ++i) to[nt][i] = im + wide[nt] + x[i];
         th[nt] = im + half[nt] + xh;
     }
-    uint32_t wd[2][2][2];
-    int ex[2][2][2];
+    uint32_t wd[2][kPer][2];
+    int ex[2][kPer][2];
     auto fetch = [&](int rd) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < kPer; ++i)
 #pragma unroll
             for (int nt = 0; nt < 2; ++nt) {
-                const int s = 2 * rd + i;
+                const int s = kPer * rd + i;
                 wd[rd & 1][i][nt] = lds32(cw + s * 256 + 128 * nt);
                 ex[rd & 1][i][nt] = lds8(ce + s * kChunk + 8 * nt);
             }
     };
     fetch(0);
 #pragma unroll
-    for (int rd = 0; rd < kSteps / 2; ++rd) {
-        uint4 a[R][4];
+    for (int rd = 0; rd < kSteps / kPer; ++rd) {
+        uint4 a[R][2 * kPer];
 #pragma unroll
         for (int r = 0; r < R; ++r)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) a[r][k] = lds128(qa + (r * kQSteps + 4 * rd + k) * 512);
-        if (rd + 1 < kSteps / 2) fetch(rd + 1);
+            for (int k = 0; k < 2 * kPer; ++k) a[r][k] = lds128(qa + (r * kQSteps + 2 * kPer * rd + k) * 512);
+        if (rd + 1 < kSteps / kPer) fetch(rd + 1);
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < kPer; ++i)
 #pragma unroll
             for (int nt = 0; nt < 2; ++nt) {
-                const int s = 2 * rd + i, j = base[nt] - ex[rd & 1][i][nt];
+                const int s = kPer * rd + i, j = base[nt] - ex[rd & 1][i][nt];
                 uint2 tab = make_uint2(tx[nt] - j * dx[nt], ty[nt] - j * dy[nt]);
                 if (kFar && dx[nt] && (j < 0 || j > kMaxJ)) tab.x = tab.y = j < 0 ? 0x7F7F7F7Fu : 0u;
                 uint32_t b0, b1;
@@ -512,8 +507,19 @@ __device__ __forceinline__ void score_role(Smem<kFp4, R>& sm, const Params& P, W
     auto mine = [&](int nt, int i) { return entry_of<kFp4>(nt, 2 * c + i); };   // the columns of this lane's scores
     int T = 0, seg = 0;
     for (; wk.left > 0; wk.next(P), ++seg) {
-        named_barrier(kBarScore, kScoreThreads);   // the last row's fragments and marks are done with
-        scale_query<kFp4, R>(sm, P, wk.b, wk.rq, warp, lane);
+        QueryPart<R> qp;
+        qp.load(P, wk.b, wk.rq, warp, g, c);
+        uint32_t top_bits[R][2];
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) top_bits[r][u] = qp.top(r, u);
+        named_barrier(kBarScore, kScoreThreads);   // the last row's fragments, marks and maxima are done with
+        if (c == 0)
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) sm.tmax[gr][w][r][g + 8 * u] = __uint_as_float(top_bits[r][u]);
         if (warp == 0) {
             if (lane < kHeads)
 #pragma unroll
@@ -521,18 +527,31 @@ __device__ __forceinline__ void score_role(Smem<kFp4, R>& sm, const Params& P, W
             if (lane == 0) sm.gs = 0.f;   // not set yet
         }
         named_barrier(kBarScore, kScoreThreads);
-        build_fragments<kFp4, R>(sm, P, wk.b, wk.rq, warp, lane);
+        float c2[R][2];   // logit factors (log2 units) of heads g, g + 8
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            float sq[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                uint32_t t = 0;
+#pragma unroll
+                for (int i = 0; i < kScoreWarps; ++i) t = max(t, __float_as_uint(sm.tmax[i >> 2][i & 3][r][g + 8 * u]));
+                const int sh = t ? max(-100, min(100, 134 - static_cast<int>(t >> 7))) : 0;
+                sq[u] = pow2f(sh);
+                c2[r][u] = P.scale * 1.4426950408889634f * pow2f(-sh);
+            }
+            qp.store(sm, r, sq, warp, lane);
+        }
         named_barrier(kBarScore, kScoreThreads);
         const int p = wk.s.n - P.Q + wk.rq / P.row_groups;   // the query's position; it sees t <= p, t > lo or t < sinks
         const int lo = P.W > 0 ? max(p, 0) - P.W : -1;
-        float nm[R][2], l[R][2], c2[R][2];   // heads g, g + 8; l is relative to nm
+        float nm[R][2], l[R][2];   // heads g, g + 8; l is relative to nm
 #pragma unroll
         for (int r = 0; r < R; ++r)
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 nm[r][k] = kUnset;
                 l[r][k] = 0.f;
-                c2[r][k] = sm.c2[r][g + 8 * k];
             }
         const int T0 = T, T1 = T + wk.len;
         for (T += (T ^ gr) & 1; T < T1; T += 2) {
@@ -1039,10 +1058,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
         Walk wk;
         wk.begin(P, b0, first, n_units);
         if (warp < kScoreWarps) {
-            regs_inc<kRegsScore<R>>();
+            regs_inc<kRegsScore>();
             score_role<kFp4, R>(sm, P, wk, warp, lane, u1, n_cta, total);
         } else if (warp < kValueWarp + kValueWarps) {
-            regs_inc<kRegsValue>();
+            regs_inc<kRegsValue<R>>();
             value_role<kFp4, R>(sm, P, wk, warp - kValueWarp, lane);
         } else {
             regs_dec<kRegsCopy<R>>();
@@ -1163,7 +1182,13 @@ size_t paged_attention_ws_bytes(int num_sms) { return num_sms * kPartBytes; }
 cudaError_t launch_paged_attention(const PagedView& c, bool fp4, const uint16_t* q, int heads, int Q, int W, int sinks,
                                    float scale, void* out, bool out_bf16, float* lse_out, void* ws, int num_sms,
                                    int32_t* err, cudaStream_t stream) {
-    const int R = heads > kHeads ? 2 : 1;   // 16-head groups of a query that a row takes together
+    // The longest row has t tiles, as far as the host knows (the window, or the capacity).
+    int64_t chunks = (c.capacity() + kChunk - 1) / kChunk;
+    if (W > 0) chunks = min64(chunks, (min64(sinks, c.capacity()) + kChunk - 1) / kChunk + (min64(W, c.capacity()) + Q - 1 + 2 * kChunk - 2) / kChunk);
+    const int64_t t = (chunks + kTileChunks - 1) / kTileChunks;
+    // Two 16-head groups a row save decoding once there is work for all SMs: 4 x 64K tokens with 64 heads, 55 tiles a CTA: fp4
+    // 171 -> 156 us, fp8 145 -> 126; but 16 windows of 4,096 with 32 heads, 7 tiles: fp4 42 -> 44, fp8 38 -> 42 (14 tiles: even).
+    const int R = heads > kHeads && (int64_t)c.batch * Q * ((heads + 2 * kHeads - 1) / (2 * kHeads)) * t >= 14 * num_sms ? 2 : 1;
     Params P;
     P.c = c;
     P.q = q;
@@ -1185,11 +1210,8 @@ cudaError_t launch_paged_attention(const PagedView& c, bool fp4, const uint16_t*
     for (int i = 0; !fp4 && i < 3; ++i)
         if (!make_tensor_map_2d_u8(&maps.rows[i], c.pages, kEntry, (uint64_t)c.n_pages * c.page_size, 128, kChunk << i))
             return cudaErrorInvalidValue;
-    // Whole rows or cut ones.  The longest row has t tiles, as far as the host knows (the window, or the capacity).
-    const int64_t rows = (int64_t)c.batch * P.rows_per_seq;
-    int64_t chunks = (c.capacity() + kChunk - 1) / kChunk;
-    if (W > 0) chunks = min64(chunks, (min64(sinks, c.capacity()) + kChunk - 1) / kChunk + (min64(W, c.capacity()) + Q - 1 + 2 * kChunk - 2) / kChunk);
-    const int64_t t = (chunks + kTileChunks - 1) / kTileChunks, n_cta = min64(num_sms, rows);
+    // Whole rows or cut ones.
+    const int64_t rows = (int64_t)c.batch * P.rows_per_seq, n_cta = min64(num_sms, rows);
     P.whole = (rows + n_cta - 1) / n_cta * t <= rows * t / num_sms + kMergeTiles;
     cudaError_t e = fp4 ? (R == 2 ? launch_rows<true, 2>(maps, P, P.whole ? n_cta : num_sms, stream)
                                   : launch_rows<true, 1>(maps, P, P.whole ? n_cta : num_sms, stream))
