@@ -573,7 +573,12 @@ csld_status kv_cache_append_paged(const csld_paged_cache* cache, const uint16_t*
     if (rope_base != 0.0 && !(rope_base > 1.0 && rope_base <= 1e300))
         return fail(CSLD_ERR_ARG, "rope_base %g: need 0 (no rotation) or a finite value above 1", rope_base);
     if (!kv_new) return fail(CSLD_ERR_ARG, "a required pointer is NULL");
-    if (start == cache->seq_len) return fail(CSLD_ERR_ARG, "start must not be the cache's seq_len; pass NULL for it");
+    // seq_len is written while start and n_new are read
+    const int32_t* len0 = cache->seq_len;
+    for (const int32_t* p : {start, n_new})
+        if (p && p < len0 + v.batch && len0 < p + v.batch)
+            return fail(CSLD_ERR_ARG, "%s must not be the cache's seq_len%s", p == start ? "start" : "n_new",
+                        p == start ? "; pass NULL for it" : "");
     if (token_stride < CSLD_DIM && T > 1) return fail(CSLD_ERR_SHAPE, "token_stride %lld below %d", (long long)token_stride, CSLD_DIM);
     if (seq_stride < 0 || token_stride < 0) return fail(CSLD_ERR_SHAPE, "a stride is negative");
     if (!aligned16(kv_new) || (seq_stride & 7) || (token_stride & 7))

@@ -423,7 +423,7 @@ typedef struct csld_paged_cache {
  * Sequence b's tokens kv_new[b][0 .. n_b), n_b = n_new ? n_new[b] : T, become the entries at
  * positions s_b .. s_b + n_b - 1, s_b = start ? start[b] : seq_len[b], and seq_len[b] = s_b + n_b.
  * (start: where a sequence goes on, e.g. behind the draft tokens that were accepted; what lay at
- * and past it is replaced or forgotten.  It must not be seq_len itself.)  rope_base > 1: dims
+ * and past it is replaced or forgotten.  Neither start nor n_new may lie over seq_len.)  rope_base > 1: dims
  * 448..511 arrive before rotary encoding and are turned at the token's position (pairs and angles
  * as in csld_compress_rope; angles reduced in double, the turn in fp32, one rounding to bf16);
  * rope_base = 0: stored as given.  All of a sequence's tokens are stored or none: if one would pass

@@ -128,3 +128,9 @@ def test_reference_attention_against_torch_softmax():
         s = (torch.from_numpy(q[0, j]) @ k.T * 0.1).masked_fill(~see, -np.inf)
         np.testing.assert_allclose(out[0, j], (torch.softmax(s, 1) @ k).numpy(), rtol=1e-12, atol=1e-12)
         np.testing.assert_allclose(lse[0, j], torch.logsumexp(s, 1).numpy(), rtol=1e-12)
+
+
+@pytest.mark.parametrize("n_new,start", [(16, None), (20, None), (12, None), (None, 20), (None, 12), (16, 64)])
+def test_append_refuses_lengths_that_lie_over_seq_len(lib, n_new, start):
+    """seq_len (two sequences, at 16) is written while n_new and start are read."""
+    assert lib.kv_cache_append_paged(C.byref(cache()), 16, 512, 512, 1, n_new, start, 0.0, None, None) == 1
