@@ -179,6 +179,79 @@ def test_attention_matches_reference(csld, fmt, lens, Q, H, page, W, sinks):
         R.assert_attention(o, l, ref, f"{fmt} {lens} Q{Q} H{H} W{W} S{sinks} {dt}")
 
 
+def _widen(csld, c, tokens):
+    """The same cache with a page table for that many tokens, the pages behind the stored ones missing. The
+    attention's way of dealing out heads follows from the capacity, so short sequences reach the long ones'."""
+    wide = np.full((c.ref.table.shape[0], tokens // c.dev.page_size), -1, np.int32)
+    wide[:, :c.ref.table.shape[1]] = c.ref.table
+    c.ref.table = wide
+    c.dev = csld.PagedCache(c.dev.pages, torch.from_numpy(wide).cuda(), c.dev.seq_len, c.dev.page_size, c.dev.fmt)
+
+
+LONG = 1 << 19   # tokens of capacity: with one query and any number of heads more than 14 tiles of 64 entries an SM
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+@pytest.mark.parametrize("lens,Q,H,page,W,sinks", [
+    ([1], 1, 32, 16, None, 0),
+    ([0, 17, 300], 1, 17, 64, None, 0),
+    ([500, 64], 2, 40, 48, None, 0),
+    ([2900, 1700], 1, 128, 64, None, 0),
+    ([90, 2, 700], 8, 24, 16, None, 0),
+    ([1300, 5], 3, 48, 32, 1 << 18, 16),
+    ([40 * i % 1201 for i in range(37)], 1, 128, 64, 1000, 4),
+])
+def test_many_heads_over_a_large_capacity(csld, fmt, lens, Q, H, page, W, sinks):
+    keep = None
+    if W is not None:
+        keep = lambda n, t: t < sinks or t > n - Q - W   # noqa: E731
+    c = Pair(csld, lens, page, fmt, seed=sum(lens) + Q + H, keep=keep)
+    _widen(csld, c, LONG // page * page)
+    q = torch.randn(len(lens), Q, H, 512, generator=synth.gen(H)).to(torch.bfloat16)
+    ref = R.attention(c.ref, q.double().numpy(), SCALE, W, sinks)
+    for dt in (torch.bfloat16, torch.float32):
+        out = torch.full(q.shape, float("nan"), dtype=dt, device="cuda")
+        if W is None:
+            o, l = csld.paged_decode_attention(c.dev, q.cuda(), SCALE, out=out)
+        else:
+            o, l = csld.paged_window_attention(c.dev, q.cuda(), W, sinks, SCALE, out=out)
+        torch.cuda.synchronize()
+        assert c.dev.err.item() == 0
+        R.assert_attention(o, l, ref, f"{fmt} {lens} Q{Q} H{H} W{W} S{sinks} {dt}")
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+@pytest.mark.parametrize("lens,H,W", [([900, 33], 32, None), ([300, 70, 5], 16, 128)])
+def test_output_in_place_of_the_query(csld, fmt, lens, H, W):
+    """out may be q: every row's query is read before its output is written, rows cut over CTAs and whole ones."""
+    c = Pair(csld, lens, 64, fmt, seed=21)
+    q = torch.randn(len(lens), 2, H, 512, generator=synth.gen(5)).to(torch.bfloat16).cuda()
+    call = (lambda x, **k: csld.paged_decode_attention(c.dev, x, SCALE, **k)) if W is None else \
+        (lambda x, **k: csld.paged_window_attention(c.dev, x, W, 4, SCALE, **k))
+    want, lw = call(q)
+    o, l = call(q, out=q)
+    assert o is q and torch.equal(o, want) and torch.equal(l, lw)
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+def test_many_heads_with_rising_and_falling_logits(csld, fmt):
+    """Heads whose running maxima move at other tiles than their neighbours', in both groups of a row."""
+    n = 1200
+    c = Pair(csld, [n], 64, fmt, seed=3)
+    d = torch.sign(torch.randn(512, generator=synth.gen(8)))
+    for t in range(n):
+        c.ref.store(0, t, (d * (t + 1) / 256.0).to(torch.bfloat16).double().numpy())
+    c.dev.pages.copy_(torch.from_numpy(c.ref.pages))
+    _widen(csld, c, LONG)
+    sign = torch.ones(32)
+    sign[5:20] = -1.0
+    sign[::7] = 0.125
+    q = (d * sign[:, None])[None, None].to(torch.bfloat16).contiguous()
+    for scale in (SCALE, 4 * SCALE):
+        o, l = csld.paged_decode_attention(c.dev, q.cuda(), scale)
+        R.assert_attention(o, l, R.attention(c.ref, q.double().numpy(), scale), f"{fmt} rising {scale}")
+
+
 @pytest.mark.parametrize("fmt", ["fp8", "fp4"])
 @pytest.mark.parametrize("scale", [8 * SCALE, -2 * SCALE, 0.0])
 def test_attention_with_peaked_flat_and_negative_scales(csld, fmt, scale):
