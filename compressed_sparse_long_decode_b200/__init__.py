@@ -654,7 +654,7 @@ def _paged_attention(what, call, cache, q, scale, out, lse, ws, err, *masks):
         raise CsldError(f"out: expected a contiguous bfloat16 or float32 tensor of shape {tuple(q.shape)}, got "
                         f"{out.dtype} {tuple(out.shape)}")
     if lse is None:
-        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+        lse = q.new_empty((cache.batch, Q, heads), dtype=torch.float32)
     elif _need(lse, torch.float32, "lse").shape != q.shape[:3]:
         raise CsldError(f"lse: expected shape {tuple(q.shape[:3])}, got {tuple(lse.shape)}")
     if ws is None:

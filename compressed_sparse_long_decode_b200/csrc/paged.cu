@@ -277,7 +277,8 @@ cudaError_t launch_append_paged(const PagedView& c, bool fp4, const uint16_t* kv
     if (rope_base > 0.0)
         for (int i = 0; i < kRope / 2; ++i)
             rt.turns[i] = std::pow(rope_base, -i / 32.0) / 6.283185307179586476925286766559;
-    // one token a warp while that leaves SMs idle (a decode step: 2.6 us of latencies either way), else four
+    // One token a warp, or four in long appends.  fp4, one token against four: 1 x 1,024 tokens 2.4 us against 3.8, 8 x 1,024
+    // 5.7 against 6.6; 12 x 1,024 7.3 against 6.7, 64 x 1,024 31.0 against 25.8 (fp8 22.5 against 19.4).
     const bool many = (int64_t)T * c.batch > 8192;
     const int per_cta = kAppendWarps * (many ? 4 : 1);
     const dim3 grid((T + per_cta - 1) / per_cta, c.batch);

@@ -343,7 +343,7 @@ struct QueryPart {
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     const int h = 16 * r + g + 8 * u;
-                    v[r][i][u] = hr + h < P.heads ? __ldg(reinterpret_cast<const uint2*>(q + h * kDim + dim_of(warp * kN + i, c)))
+                    v[r][i][u] = hr + h < P.heads ? __ldcg(reinterpret_cast<const uint2*>(q + h * kDim + dim_of(warp * kN + i, c)))
                                                   : make_uint2(0, 0);
                 }
     }
@@ -598,11 +598,15 @@ __device__ __forceinline__ void score_role(Smem<kFp4, R>& sm, const Params& P, W
                 for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) fe[nt][i] = (vis >> mine(nt, i)) & 1 ? 1.f : 0.f;
-                if (vis != 0xFFFFu) {   // masked rows are zeroed for the value warps
-                    for (int en = 0; en < 16; ++en)
+                if (vis != 0xFFFFu) {   // masked rows are zeroed for the value warps, eight lanes a row
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int en = 4 * i + (lane >> 3);
                         if (!((vis >> en) & 1))
-                            for (int k = lane; k < 40; k += 32)
-                                *reinterpret_cast<uint4*>(img + (k >> 3) * kBlkBytes + sw128(16 * w + en, 16 * (k & 7))) = make_uint4(0, 0, 0, 0);
+#pragma unroll
+                            for (int k = 0; k < 5; ++k)
+                                *reinterpret_cast<uint4*>(img + k * kBlkBytes + sw128(16 * w + en, 16 * (lane & 7))) = make_uint4(0, 0, 0, 0);
+                    }
                     fence_proxy_async_smem();   // the ring's next copy writes there too
                     __syncwarp();
                 }

@@ -454,7 +454,7 @@ CSLD_API csld_status kv_cache_read_paged(const csld_paged_cache* cache, const in
  * page is outside 0..n_pages-1 its tokens are left out and CSLD_DEVERR_PAGE is set.  What lies in
  * masked places (behind a sequence's end, outside the window) may be anything, NaN included.
  *   q [batch][Q][heads][512] bf16; out the same shape, fp32 (out_type CSLD_OUT_F32) or bf16
- *   (CSLD_OUT_BF16); lse_out [batch][Q][heads] f32 or NULL; 1 <= heads <= CSLD_PAGED_MAX_HEADS,
+ *   (CSLD_OUT_BF16; then q itself may be out); lse_out [batch][Q][heads] f32 or NULL; 1 <= heads <= CSLD_PAGED_MAX_HEADS,
  *   1 <= Q <= CSLD_MULTI_MAX_Q, 1 <= W, 0 <= sinks; q, out, ws 16-byte aligned.
  * Products: the bf16 query against the stored codes exactly (down to 2^-21 of a head's largest value),
  * softmax weights rounded to f16 (2^-11) for the 8- and 4-bit dims and to bf16 for the RoPE dims; sums and
