@@ -43,11 +43,12 @@
 //   value  (warps 8-15) warp w owns 64 of the 512 dims and keeps its O in registers: O += P V, V fragments by
 //                       transposing 8-bit matrix loads of the image (fp8: of the copied tile itself); the last warp the
 //                       RoPE dims, bf16
-// Where a query has more than 16 heads a row is two groups of 16 (R = 2): keys are decoded and values loaded once for both.
+// Where a query has more than 16 heads and there is work for all SMs a row is two groups of 16 (R = 2): keys are decoded
+// and values loaded once for both.
 //
 // What bounds it (fp4, R = 1, a 64-entry tile, 1M tokens; cycles an SM): HBM 975; f16 MMAs 1,024; ALU (permutes, masks) 1,040;
 // shared memory about 1,700 wavefronts; 6,500 instructions, 1,630 a scheduler; taken: 2,630, 0.6 instructions a cycle
-// and scheduler.  176 us, 2.2 TB/s, 0.34 of the copy rate.  fp8: 86 us for 8 x 64K tokens, 3.5 TB/s, 0.53.
+// and scheduler.  176 us, 2.2 TB/s, 0.34 of the copy rate.  fp8: 84 us for 8 x 64K tokens, 3.6 TB/s, 0.55.
 // A third score group (with four value warps of 128 dims) gave 181 us, more or larger stages nothing.
 // Rows of masked or missing tokens are zeroed before they are used, whatever was in them.  The waits for copies are
 // bounded; one that gives up sets CSLD_DEVERR_TIMEOUT and all roles run out without waiting for copies.
@@ -598,15 +599,13 @@ __device__ __forceinline__ void score_role(Smem<kFp4, R>& sm, const Params& P, W
                 for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) fe[nt][i] = (vis >> mine(nt, i)) & 1 ? 1.f : 0.f;
-                if (vis != 0xFFFFu) {   // masked rows are zeroed for the value warps, eight lanes a row
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int en = 4 * i + (lane >> 3);
+                if (vis != 0xFFFFu) {   // masked rows are zeroed for the value warps, eight lanes a row (unrolled, the full tiles lose 2 %)
+#pragma unroll 1
+                    for (int en = lane >> 3; en < 16; en += 4)
                         if (!((vis >> en) & 1))
 #pragma unroll
                             for (int k = 0; k < 5; ++k)
                                 *reinterpret_cast<uint4*>(img + k * kBlkBytes + sw128(16 * w + en, 16 * (lane & 7))) = make_uint4(0, 0, 0, 0);
-                    }
                     fence_proxy_async_smem();   // the ring's next copy writes there too
                     __syncwarp();
                 }
