@@ -731,13 +731,15 @@ __device__ __forceinline__ void score_role(Smem<kFp4, R>& sm, const Params& P, W
         }
         T = T1;
         // ---- the segment's sums, relative to the last marks --------------------------------------------
-        if (((T1 - 1) & 1) != gr) bar_sync(kBarMark + ((T1 - 1) & 1), kScoreThreads);
+        // The group of the last tile has the marks in registers: its warps have not met since warp 0 of it may have stored them.
+        const bool last_own = ((T1 - 1) & 1) == gr;
+        if (!last_own) bar_sync(kBarMark + ((T1 - 1) & 1), kScoreThreads);
         if (seg >= 1) bar_sync(kBarSegFree, kScoreThreads + kValueThreads);
 #pragma unroll
         for (int r = 0; r < R; ++r)
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                const float mk = sm.nm[r][g + 8 * k];
+                const float mk = last_own ? nm[r][k] : sm.nm[r][g + 8 * k];
                 float v = mk != nm[r][k] ? l[r][k] * exp2_ftz(mk - nm[r][k]) : l[r][k];
                 v += __shfl_xor_sync(0xffffffffu, v, 1);
                 v += __shfl_xor_sync(0xffffffffu, v, 2);

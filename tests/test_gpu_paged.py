@@ -543,3 +543,32 @@ def test_binding_refuses_bad_tensors(csld):
             call()
     torch.cuda.synchronize()
     assert c.err.item() == 0 and c.seq_len.sum().item() == 0
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+@pytest.mark.parametrize("rising", [False, True])
+def test_sums_of_rows_whose_last_tile_sets_the_marks(csld, fmt, rising):
+    """Rows of one tile, whose only tile sets the marks that its sums are relative to, and rows of a few tiles with
+    rising logits, whose last one moves them: the sums of all four warps of the tile's group go by the
+    new marks, in every one of many calls."""
+    rng = np.random.default_rng(17)
+    lens = [int(n) for n in rng.integers(1, 65 if not rising else 290, 100 if not rising else 24)]
+    c = Pair(csld, lens, 64, fmt, seed=41)
+    d = torch.sign(torch.randn(512, generator=synth.gen(8)))
+    if rising:
+        for b, n in enumerate(lens):
+            for t in range(n):
+                c.ref.store(b, t, (d * (t + 1) / 64.0).to(torch.bfloat16).double().numpy())
+        c.dev.pages.copy_(torch.from_numpy(c.ref.pages))
+        q = (d * torch.tensor([1.0, -1.0, 0.5, 0.25] * 4)[:, None]).expand(len(lens), 1, 16, 512).to(torch.bfloat16).contiguous()
+    else:
+        q = torch.randn(len(lens), 1, 16, 512, generator=synth.gen(6)).to(torch.bfloat16)
+    ref, qd = R.attention(c.ref, q.double().numpy(), SCALE), q.cuda()
+    first = [t.clone() for t in csld.paged_decode_attention(c.dev, qd, SCALE)]
+    R.assert_attention(*first, ref, f"{fmt} {rising}")
+    out, lse, same = torch.empty_like(first[0]), torch.empty_like(first[1]), torch.ones((), dtype=torch.bool, device="cuda")
+    ws = csld.paged_attention_workspace()
+    for _ in range(300):
+        csld.paged_decode_attention(c.dev, qd, SCALE, out=out, lse=lse, ws=ws)
+        same &= (out == first[0]).all() & (lse == first[1]).all()
+    assert same.item() and c.dev.err.item() == 0
