@@ -955,6 +955,7 @@ __device__ __forceinline__ void copy_role(Smem<kFp4, R>& sm, const Params& P, Wa
                 }
                 if (ck < kTileChunks && (kFp4 || blk == 0)) sm.chunk_tok[st][ck] = tok;
                 const int n = __popc(__ballot_sync(0xffffffffu, mine));
+                __syncwarp();   // orders the lanes' chunk_tok before lane 0's arrive, which is all there is for a tile without chunks
                 if (lane == 0) {
                     sm.n_issued = T + 1;
                     mbar_arrive_expect_tx(&sm.full[st], n * (kFp4 ? kChunk4Bytes : kChunk * 128));

@@ -572,3 +572,21 @@ def test_sums_of_rows_whose_last_tile_sets_the_marks(csld, fmt, rising):
         csld.paged_decode_attention(c.dev, qd, SCALE, out=out, lse=lse, ws=ws)
         same &= (out == first[0]).all() & (lse == first[1]).all()
     assert same.item() and c.dev.err.item() == 0
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+def test_tiles_without_a_chunk_after_full_ones(csld, fmt):
+    """Rows that follow one another in a CTA's share and take turns between full tiles, empty sequences and tiles
+    whose pages are all missing: nothing of a ring slot's earlier tile counts for a tile that copies nothing."""
+    lens = [0 if b % 3 == 1 else 64 + 64 * (b % 4) + b % 5 for b in range(12)]
+    c = Pair(csld, lens, 64, fmt, seed=43)
+    for b in range(0, 12, 4):
+        c.ref.table[b, 1:] = -1 if b else 10 ** 6      # all but the first tile of these rows lost
+    c.dev.page_table.copy_(torch.from_numpy(c.ref.table))
+    reps = 40                                          # 480 rows: every CTA walks several
+    dev = csld.PagedCache(c.dev.pages, c.dev.page_table.repeat(reps, 1), c.dev.seq_len.repeat(reps), 64, fmt)
+    q = torch.randn(12, 1, 16, 512, generator=synth.gen(6)).to(torch.bfloat16)
+    o, l = csld.paged_decode_attention(dev, q.repeat(reps, 1, 1, 1).cuda(), SCALE)
+    ref = R.attention(c.ref, q.double().numpy(), SCALE)
+    R.assert_attention(o, l, [np.tile(a, (reps,) + (1,) * (a.ndim - 1)) for a in ref], fmt)
+    assert dev.err.item() == 16
