@@ -72,12 +72,14 @@ __global__ void __launch_bounds__(32 * kAppendWarps) append_paged_kernel(
     const int i0 = blockIdx.x * kAppendWarps * kTokens + warp;
     uint4 va[kTokens], vb[kTokens];
     uint32_t vr[kTokens];
+    // rows past n_new are not read: where sequences lie closer than T rows they may end the caller's buffer
+    const int n_in = n_new ? n_new[b] : T, n_rows = n_in <= T ? n_in : 0;
 #pragma unroll
-    for (int k = 0; k < kTokens; ++k) {   // rows past n_new are read too (they are the caller's padding), never stored
+    for (int k = 0; k < kTokens; ++k) {
         const int i = i0 + k * kAppendWarps;
         va[k] = vb[k] = make_uint4(0, 0, 0, 0);
         vr[k] = 0;
-        if (i < T) {
+        if (i < n_rows) {
             const uint16_t* x = kv_new + b * seq_stride + i * token_stride;
             if (lane < 28) {
                 va[k] = __ldg(reinterpret_cast<const uint4*>(x) + 2 * lane);

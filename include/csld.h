@@ -431,7 +431,8 @@ typedef struct csld_paged_cache {
  * of that sequence changes and CSLD_DEVERR_CAPACITY, _PAGE or _SEQ_LEN is ORed into *err.  Nothing
  * but those entries is written.
  *   kv_new: token i of sequence b at kv_new + b * seq_stride + i * token_stride (elements, multiples
- *   of 8), 512 bf16 each, 16-byte aligned; n_new, start [batch] device int32 or NULL; 1 <= T <= 2^20. */
+ *   of 8), 512 bf16 each, 16-byte aligned; only the tokens below n_b are read, so sequences may lie closer
+ *   than T tokens, and the last one may end with its n_b; n_new, start [batch] device int32 or NULL; 1 <= T <= 2^20. */
 CSLD_API csld_status kv_cache_append_paged(const csld_paged_cache* cache, const uint16_t* kv_new, int64_t seq_stride,
                                            int64_t token_stride, int T, const int32_t* n_new, const int32_t* start,
                                            double rope_base, int32_t* err, void* stream);

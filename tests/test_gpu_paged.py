@@ -590,3 +590,32 @@ def test_tiles_without_a_chunk_after_full_ones(csld, fmt):
     ref = R.attention(c.ref, q.double().numpy(), SCALE)
     R.assert_attention(o, l, [np.tile(a, (reps,) + (1,) * (a.ndim - 1)) for a in ref], fmt)
     assert dev.err.item() == 16
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+@pytest.mark.parametrize("T,n", [(4, [1, 0, 1]), (3000, [5, 2, 0, 7])])
+def test_append_reads_only_the_tokens_that_there_are(csld, fmt, T, n):
+    """Sequences that lie right behind one another in the caller's buffer, closer than T tokens, the last ending with it;
+    a refused count (T + 1, -1) reads nothing."""
+    gap = max(n)
+    c = Pair(csld, [3] * len(n), 32, fmt, seed=44, extra=T)
+    x = _tokens(synth.gen(9), len(n), gap)
+    n_new = torch.tensor(n, dtype=torch.int32)
+    rows = (len(n) - 1) * gap + n[-1]            # up to the last sequence's last token
+    buf = x.view(-1, 512)[:rows].contiguous().cuda()
+
+    def call(counts):
+        counts = counts.cuda()
+        assert csld.lib.kv_cache_append_paged(c.dev._ref, buf.data_ptr(), gap * 512, 512, T, counts.data_ptr(), None, BASE,
+                                              c.dev.err.data_ptr(), torch.cuda.current_stream().cuda_stream) == 0
+        torch.cuda.synchronize()
+
+    call(n_new)
+    full = np.zeros((len(n), T, 512))
+    full[:, :gap] = x.double().numpy()
+    c.ref.append(full, n_new.numpy(), None, BASE)
+    c.check_bytes(rope_ulp=1)
+    assert c.dev.err.item() == 0
+    before = c.dev.pages.clone()
+    call(torch.tensor([T + 1, -1] + [0] * (len(n) - 2), dtype=torch.int32))
+    assert c.dev.err.item() == 4 and torch.equal(before, c.dev.pages)
