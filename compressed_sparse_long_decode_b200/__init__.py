@@ -538,33 +538,50 @@ class PagedCache:
     torch: pages [n_pages, page_size * entry bytes] u8, page_table [B, max_pages] i32 (the page of
     token t: page_table[b, t // page_size]), seq_len [B] i32; fmt "fp8" (576-byte entries) or "fp4"
     (368 bytes per token).  The tensors are the caller's to fill and keep; page_table and seq_len may
-    be changed in place between calls, err collects the device flags."""
+    be changed in place between calls, err collects the device flags.  Another tensor assigned to pages,
+    page_table, seq_len or err is checked as at construction and taken by the next call (a tensor given
+    other storage by set_ or resize_ is not followed: assign it again); what follows from them (batch,
+    max_pages, n_pages, ..) and the format cannot be assigned."""
 
     FORMATS = {"fp8": (8, ENTRY_BYTES), "fp4": (4, ENTRY_FP4_BYTES)}
 
     def __init__(self, pages, page_table, seq_len, page_size, fmt="fp8", err=None):
         if fmt not in self.FORMATS:
             raise CsldError(f"fmt: expected one of {sorted(self.FORMATS)}, got {fmt!r}")
+        self.__dict__.update(fmt=fmt, page_size=page_size, entry_bytes=self.FORMATS[fmt][1])
+        self._take(pages, page_table, seq_len)
+        self.err = torch.zeros(1, dtype=torch.int32, device=self.device) if err is None else err
+
+    def _take(self, pages, page_table, seq_len):
+        """Checks the tensors and forms what the calls hand to the library."""
         _need(pages, torch.uint8, "pages")
         _need(page_table, torch.int32, "page_table")
         _need(seq_len, torch.int32, "seq_len")
-        code, entry = self.FORMATS[fmt]
         if page_table.dim() != 2 or seq_len.shape != page_table.shape[:1]:
             raise CsldError(f"page_table {tuple(page_table.shape)} and seq_len {tuple(seq_len.shape)}: expected "
                             "[B, max_pages] and [B]")
-        if pages.dim() < 2 or pages.numel() != pages.shape[0] * page_size * entry:
-            raise CsldError(f"pages {tuple(pages.shape)}: expected [n_pages, page_size * {entry}] bytes")
+        if pages.dim() < 2 or pages.numel() != pages.shape[0] * self.page_size * self.entry_bytes:
+            raise CsldError(f"pages {tuple(pages.shape)}: expected [n_pages, page_size * {self.entry_bytes}] bytes")
         if not pages.device == page_table.device == seq_len.device:
             raise CsldError("pages, page_table and seq_len lie on different devices")
-        self.fmt, self.page_size, self.entry_bytes = fmt, page_size, entry
-        self.pages, self.page_table, self.seq_len = pages, page_table, seq_len
-        self.batch, self.max_pages, self.n_pages = page_table.shape[0], page_table.shape[1], pages.shape[0]
-        self.device = pages.device
-        self.err = torch.zeros(1, dtype=torch.int32, device=self.device) if err is None else _need(err, torch.int32, "err")
-        self._struct = _Paged(code, page_size, self.batch, self.max_pages, self.n_pages, pages.data_ptr(),
-                              page_table.data_ptr(), seq_len.data_ptr())
-        self._ref = C.byref(self._struct)
-        self._index = pages.get_device()
+        batch, max_pages, n_pages = page_table.shape[0], page_table.shape[1], pages.shape[0]
+        struct = _Paged(self.FORMATS[self.fmt][0], self.page_size, batch, max_pages, n_pages, pages.data_ptr(),
+                        page_table.data_ptr(), seq_len.data_ptr())
+        self.__dict__.update(pages=pages, page_table=page_table, seq_len=seq_len, batch=batch, max_pages=max_pages,
+                             n_pages=n_pages, device=pages.device, _struct=struct, _ref=C.byref(struct),
+                             _index=pages.get_device())
+
+    def __setattr__(self, name, value):
+        if name in ("pages", "page_table", "seq_len"):
+            self._take(**{**{k: self.__dict__[k] for k in ("pages", "page_table", "seq_len")}, name: value})
+        elif name == "err":
+            if _need(value, torch.int32, "err").device != self.device:
+                raise CsldError(f"err is on {value.device}, the cache on {self.device}")
+            self.__dict__["err"] = value
+        elif name in self.__dict__:
+            raise CsldError(f"{name} of a PagedCache cannot be assigned; make another one")
+        else:
+            super().__setattr__(name, value)
 
     def _stream(self):
         return torch._C._cuda_getCurrentRawStream(self._index)

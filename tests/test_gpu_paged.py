@@ -619,3 +619,43 @@ def test_append_reads_only_the_tokens_that_there_are(csld, fmt, T, n):
     before = c.dev.pages.clone()
     call(torch.tensor([T + 1, -1] + [0] * (len(n) - 2), dtype=torch.int32))
     assert c.dev.err.item() == 4 and torch.equal(before, c.dev.pages)
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+def test_tensors_assigned_to_a_cache_are_the_ones_that_calls_use(csld, fmt):
+    c = Pair(csld, [70, 20], 32, fmt, seed=45)
+    q = torch.randn(2, 1, 16, 512, generator=synth.gen(6)).to(torch.bfloat16)
+    old = [c.dev.pages, c.dev.page_table, c.dev.seq_len]
+    was = [t.clone() for t in old]
+    c.ref.seq_len[:] = [33, 20]
+    c.dev.seq_len = torch.tensor([33, 20], dtype=torch.int32).cuda()
+    o, l = csld.paged_decode_attention(c.dev, q.cuda(), SCALE)
+    R.assert_attention(o, l, R.attention(c.ref, q.double().numpy(), SCALE), f"{fmt} lengths")
+    # a longer table over a pool of its own
+    c.ref.pages = np.concatenate([c.ref.pages, np.full_like(c.ref.pages[:2], 0xFF)])[::-1].copy()
+    c.ref.n_pages += 2
+    c.ref.table = np.concatenate([c.ref.n_pages - 1 - c.ref.table, np.array([[0], [1]], np.int32)], 1)
+    c.dev.pages = torch.from_numpy(c.ref.pages.copy()).cuda()
+    c.dev.page_table = torch.from_numpy(c.ref.table).cuda()
+    c.dev.err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    assert (c.dev.max_pages, c.dev.n_pages) == (c.ref.table.shape[1], c.ref.n_pages)
+    x = _tokens(synth.gen(3), 2, 50)
+    csld.kv_cache_append_paged(c.dev, x.cuda())
+    c.ref.append(x.double().numpy(), None, None, 0.0)
+    c.check_bytes()
+    o, l = csld.paged_decode_attention(c.dev, q.cuda(), SCALE)
+    R.assert_attention(o, l, R.attention(c.ref, q.double().numpy(), SCALE), f"{fmt} pages")
+    assert c.dev.err.item() == 0 and all(torch.equal(a, b) for a, b in zip(old, was))
+
+
+def test_a_cache_refuses_what_does_not_fit_it(csld):
+    c = csld.PagedCache.allocate(2, 100, 16, "fp4")
+    have = dict(c.__dict__)
+    for name, bad in (("seq_len", torch.zeros(3, dtype=torch.int32, device="cuda")), ("seq_len", c.seq_len.long()),
+                      ("seq_len", c.seq_len.cpu()), ("page_table", c.page_table[0]), ("page_table", c.page_table.t()),
+                      ("pages", c.pages[:, :-16]), ("pages", c.pages.view(torch.int8)), ("err", torch.zeros(1, device="cuda")),
+                      ("err", torch.zeros(1, dtype=torch.int32)), ("batch", 1), ("max_pages", 1), ("n_pages", 1), ("page_size", 32),
+                      ("fmt", "fp8"), ("entry_bytes", 576), ("device", torch.device("cpu")), ("_struct", None), ("_ref", None)):
+        with pytest.raises(csld.CsldError):
+            setattr(c, name, bad)
+    assert c.__dict__ == have
