@@ -676,6 +676,8 @@ def _paged_attention(what, call, cache, q, scale, out, lse, ws, err, *masks):
         raise CsldError(f"lse: expected shape {tuple(q.shape[:3])}, got {tuple(lse.shape)}")
     if ws is None:
         ws = paged_attention_workspace(q.device)
+    elif not ws.is_contiguous():
+        raise CsldError(f"ws: expected a contiguous tensor, got {tuple(ws.shape)} strides {ws.stride()}")
     err = cache.err if err is None else _need(err, torch.int32, "err")
     _on_device(cache, what, q, out, lse, ws, err)
     _check(call(cache._ref, q.data_ptr(), heads, Q, *masks, scale, out.data_ptr(), int(out.dtype == torch.bfloat16),

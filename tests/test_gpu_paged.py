@@ -659,3 +659,18 @@ def test_a_cache_refuses_what_does_not_fit_it(csld):
         with pytest.raises(csld.CsldError):
             setattr(c, name, bad)
     assert c.__dict__ == have
+
+
+def test_workspaces_that_are_no_plain_memory_are_refused(csld):
+    """A view whose elements lie apart, or one element many times, has fewer bytes in a row than it counts."""
+    c = csld.PagedCache.allocate(2, 100, 16, "fp4")
+    q = torch.zeros(2, 1, 16, 512, dtype=torch.bfloat16, device="cuda")
+    n = csld.paged_attention_workspace().numel()
+    for ws in (torch.zeros(1, dtype=torch.uint8, device="cuda").expand(n), torch.zeros(n // 16, 32, dtype=torch.uint8, device="cuda")[:, :16],
+               torch.zeros(n, dtype=torch.uint8)):
+        for call in (lambda: csld.paged_decode_attention(c, q, SCALE, ws=ws),
+                     lambda: csld.paged_window_attention(c, q, 8, 4, SCALE, ws=ws)):
+            with pytest.raises(csld.CsldError):
+                call()
+    torch.cuda.synchronize()
+    assert c.err.item() == 0
