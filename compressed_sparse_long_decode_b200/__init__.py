@@ -567,6 +567,8 @@ class PagedCache:
         batch, max_pages, n_pages = page_table.shape[0], page_table.shape[1], pages.shape[0]
         struct = _Paged(self.FORMATS[self.fmt][0], self.page_size, batch, max_pages, n_pages, pages.data_ptr(),
                         page_table.data_ptr(), seq_len.data_ptr())
+        if page_table is not self.__dict__.get("page_table"):
+            self.__dict__.update(ring_tokens=None, _ring=None)   # allocate's, of the table that it made
         self.__dict__.update(pages=pages, page_table=page_table, seq_len=seq_len, batch=batch, max_pages=max_pages,
                              n_pages=n_pages, device=pages.device, _struct=struct, _ref=C.byref(struct),
                              _index=pages.get_device())
@@ -590,20 +592,32 @@ class PagedCache:
     def allocate(cls, batch, context, page_size=64, fmt="fp8", device="cuda", window=None, sinks=0, new_tokens=8):
         """An empty cache with room for `context` tokens of each sequence, its pages dealt out in order.
         window: for paged_window_attention alone, with that window and `sinks` first tokens and at most
-        new_tokens appended or attended at a time: behind the first tokens' pages the same few pages
-        take turns, so a sequence holds window + sinks tokens (and a page or two) whatever the context."""
+        new_tokens decoded (appended, attended, or taken back by `start`) at a time: behind the first tokens'
+        pages the same few pages take turns, so a sequence holds window + sinks tokens (and a page or two)
+        whatever the context.  The cache's ring_tokens says how many of the newest tokens these pages keep
+        (None: every token has its own place); what would need a token that they no longer hold, or more
+        places than there are, is refused: appends of more than ring_tokens tokens, wider windows or more
+        first tokens, paged_decode_attention.  A longer prompt goes in as its first `sinks` tokens with start 0
+        (ring_tokens at most at a time), then its last ring_tokens (or fewer, window + new_tokens - 1 at least)
+        with start at the position of the first of these.  A read-back gives such a token's place as it is now."""
         per = max(1, -(-context // page_size))
         dev = torch.device(device)
         entry = cls.FORMATS[fmt][1] if fmt in cls.FORMATS else 0
         held = torch.arange(per, dtype=torch.int32, device=dev)
+        limits = None
         if window is not None:
             first = -(-sinks // page_size)
             ring = (window + 2 * new_tokens + page_size - 3) // page_size + 1   # pages that so many tokens in a row may touch
             held = torch.where(held < first, held, first + (held - first) % ring)
+            if per > first + ring:
+                limits = dict(ring_tokens=ring * page_size, _ring=(window, sinks, new_tokens))
         n = int(held.max()) + 1
         table = held[None, :] + n * torch.arange(batch, dtype=torch.int32, device=dev)[:, None]
-        return cls(torch.zeros((batch * n, page_size * entry), dtype=torch.uint8, device=dev), table.contiguous(),
-                   torch.zeros(batch, dtype=torch.int32, device=dev), page_size, fmt)
+        cache = cls(torch.zeros((batch * n, page_size * entry), dtype=torch.uint8, device=dev), table.contiguous(),
+                    torch.zeros(batch, dtype=torch.int32, device=dev), page_size, fmt)
+        if limits:
+            cache.__dict__.update(limits)
+        return cache
 
 
 def _on_device(cache, what, *tensors):
@@ -631,6 +645,9 @@ def kv_cache_append_paged(cache: PagedCache, kv_new, n_new=None, start=None, rop
     T = kv_new.shape[1]
     if T == 0:
         raise CsldError("kv_new: no tokens")
+    if cache.ring_tokens is not None and T > cache.ring_tokens:
+        raise CsldError(f"kv_new: {T} tokens at a time, but the cache's window keeps only the newest {cache.ring_tokens} "
+                        "(PagedCache.allocate tells how a prompt goes in)")
     # the stride of a dimension of length 1 is never used
     _check(lib.kv_cache_append_paged(cache._ref, kv_new.data_ptr(), kv_new.stride(0) if cache.batch > 1 else 0,
                                      kv_new.stride(1) if T > 1 else 0, T, _ptr(n_new), _ptr(start), rope_base,
@@ -688,6 +705,8 @@ def _paged_attention(what, call, cache, q, scale, out, lse, ws, err, *masks):
 def paged_decode_attention(cache: PagedCache, q, scale, out=None, lse=None, ws=None, err=None):
     """The Q newest tokens of each sequence over all tokens up to their own: q [B,Q,heads,512] bf16 ->
     (out [B,Q,heads,512] bf16, or fp32 where such an `out` is given; lse [B,Q,heads] f32)."""
+    if cache._ring is not None:
+        raise CsldError(f"paged_decode_attention: the cache was allocated for a window of {cache._ring[0]} and holds no older tokens")
     return _paged_attention("paged_decode_attention", lib.paged_decode_attention, cache, q, scale, out, lse, ws, err)
 
 
@@ -696,6 +715,11 @@ def paged_window_attention(cache: PagedCache, q, W, sinks, scale, out=None, lse=
     for v, name in ((W, "W"), (sinks, "sinks")):
         if not 0 <= v <= 0x7FFFFFFF:
             raise CsldError(f"{name} {v} outside 0..2^31-1")
+    if cache._ring is not None:
+        window, first, new = cache._ring
+        if sinks > first or (q.dim() == 4 and W + q.shape[1] > window + new):
+            raise CsldError(f"paged_window_attention: the cache was allocated for a window of {window}, {first} first tokens and {new} "
+                            f"new ones at a time, not for W {W}, sinks {sinks}, q {tuple(q.shape)}")
     return _paged_attention("paged_window_attention", lib.paged_window_attention, cache, q, scale, out, lse, ws, err,
                             W, sinks)
 

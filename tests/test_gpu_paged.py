@@ -674,3 +674,64 @@ def test_workspaces_that_are_no_plain_memory_are_refused(csld):
                 call()
     torch.cuda.synchronize()
     assert c.err.item() == 0
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+@pytest.mark.parametrize("page,window,sinks,new", [(16, 40, 5, 4), (64, 32, 0, 1), (32, 64, 40, 8)])
+def test_a_prompt_into_a_window_cache(csld, fmt, page, window, sinks, new):
+    """Prompts of several lengths through a ring that is shorter than they are, as the documentation says: the first tokens,
+    then the last ring_tokens; then draft steps of which some tokens are taken back.  The reference keeps every token."""
+    B, context = 3, 400
+    dev = csld.PagedCache.allocate(B, context, page, fmt, window=window, sinks=sinks, new_tokens=new)
+    k = dev.ring_tokens
+    assert window + 2 * new - 2 <= k < context - sinks
+    per = -(-context // page)
+    ref = R.Cache(np.zeros((B * per, page * R.ENTRY[fmt]), np.uint8), np.arange(B * per, dtype=np.int32).reshape(B, per),
+                  np.zeros(B, np.int32), page, fmt)
+    lens = [300, k + 3, 17]
+    g = synth.gen(46)
+    x = _tokens(g, B, 300)
+    if sinks:
+        csld.kv_cache_append_paged(dev, x[:, :sinks].cuda())
+    start = [max(0, n - k) for n in lens]
+    tail = torch.zeros(B, k, 512, dtype=torch.bfloat16)
+    for b, n in enumerate(lens):
+        tail[b, :n - start[b]] = x[b, start[b]:n]
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")   # noqa: E731
+    csld.kv_cache_append_paged(dev, tail.cuda(), n_new=i32([n - s for n, s in zip(lens, start)]), start=i32(start))
+    ref.append(x.double().numpy(), lens, None, 0.0)
+    at = list(lens)
+    for step in range(6):
+        hx, q = _tokens(g, B, new), torch.randn(B, new, 16, 512, generator=g).to(torch.bfloat16)
+        csld.kv_cache_append_paged(dev, hx.cuda(), start=i32(at))
+        ref.append(hx.double().numpy(), None, at, 0.0)
+        o, l = csld.paged_window_attention(dev, q.cuda(), window, sinks, SCALE)
+        R.assert_attention(o, l, R.attention(ref, q.double().numpy(), SCALE, window, sinks), f"{fmt} step {step}")
+        at = [n + max(0, new - 1 - (step + b) % 3) for b, n in enumerate(at)]
+    assert dev.err.item() == 0
+
+
+def test_window_caches_refuse_what_they_do_not_hold(csld):
+    c = csld.PagedCache.allocate(2, 400, 16, "fp4", window=40, sinks=5, new_tokens=2)
+    k = c.ring_tokens
+    q = torch.zeros(2, 2, 16, 512, dtype=torch.bfloat16, device="cuda")
+    x = torch.zeros(2, k + 1, 512, dtype=torch.bfloat16, device="cuda")
+    for call in (lambda: csld.kv_cache_append_paged(c, x), lambda: csld.kv_cache_append_paged(c, x, n_new=c.seq_len + 1),
+                 lambda: csld.paged_decode_attention(c, q, SCALE), lambda: csld.paged_window_attention(c, q, 41, 5, SCALE),
+                 lambda: csld.paged_window_attention(c, q, 40, 6, SCALE),
+                 lambda: csld.paged_window_attention(c, q.repeat(1, 2, 1, 1), 40, 5, SCALE)):
+        with pytest.raises(csld.CsldError):
+            call()
+    torch.cuda.synchronize()
+    assert c.err.item() == 0 and c.seq_len.sum().item() == 0
+    csld.kv_cache_append_paged(c, x[:, :k])
+    csld.paged_window_attention(c, q, 40, 5, SCALE)
+    csld.paged_window_attention(c, q.repeat(1, 2, 1, 1), 38, 0, SCALE)
+    # a table of the caller's, and a ring that never turns, have no such limits
+    whole = csld.PagedCache.allocate(2, 60, 16, "fp4", window=40, sinks=5, new_tokens=2)
+    assert whole.ring_tokens is None
+    c.page_table = whole.page_table
+    assert c.ring_tokens is None
+    csld.paged_decode_attention(whole, q, SCALE)
+    torch.cuda.synchronize()
+    assert c.err.item() == 0 and whole.err.item() == 0
