@@ -38,8 +38,9 @@
 //                       over one power of two f_e, applied to S and to P.  They also go to the value image.  fp8: the
 //                       hardware's E4M3 -> f16 converts.  Then the softmax: p relative to a mark nm that is raised only
 //                       when some p exceeds it by 2^10, the marks handed from tile to tile, one meeting of the
-//                       four warps a tile, and P as A fragments in shared memory: p f_e g in f16 (2^-11), for the RoPE
-//                       dims p in bf16.
+//                       four warps a tile, and P as A fragments in shared memory: in f16 (2^-11) p, fp4 p f_e 2^dm with a
+//                       second mark dm that follows a head's largest p f_e, so that an entry far larger than those
+//                       that carry the weight costs them nothing; for the RoPE dims p in bf16.
 //   value  (warps 8-15) warp w owns 64 of the 512 dims and keeps its O in registers: O += P V, V fragments by
 //                       transposing 8-bit matrix loads of the image (fp8: of the copied tile itself); the last warp the
 //                       RoPE dims, bf16
@@ -79,12 +80,15 @@ constexpr int kImgBytes = 4 * kBlkBytes + kBlkBytes / 2;
 template <bool kFp4> constexpr int kRopeAt = kFp4 ? 3 * kBlkBytes + kBlkBytes / 2 : 4 * kBlkBytes;
 constexpr int kSteps = kGroups;                  // 32-dim steps of the 448 dims
 constexpr int kQSteps = 2 * kSteps + 4;          // 16-dim MMA steps of the query, the RoPE ones last
-// Marks: a head's nm is set so that the largest p of a tile is 2^kLift and kept until one exceeds 2^kOver.  The
-// operand holds p w in f16, w = 1 (fp8) or f_e g (fp4; g a power of two set so that the tile's largest f_e g is
-// kFeSet, kept until one exceeds kFeMost).  f16 bounds the product: 2^kOver w <= 2^15.
+// Marks: a head's nm is set so that the largest p of a tile is 2^kLift and kept until one exceeds 2^kOver.  The f16
+// operand holds w = p (fp8), or w = p f_e 2^dm (fp4), dm a whole number per head: set so that the tile's largest w lies in
+// 2^(kLiftW - 1) .. 2^kLiftW, moved against nm when that moves (w stays as it was, but for a fraction er of a bit that is
+// carried along, at most 1/2), and set anew when some w exceeds 2^kOverW.  So a w of 2^-18 of the head's largest keeps
+// f16's 11 bits, and no w is off by more than 2^-29 of the largest.
 template <bool kFp4> constexpr float kLift = kFp4 ? 0.f : 5.f;
 template <bool kFp4> constexpr float kOver = kFp4 ? 10.f : 15.f;
-constexpr float kFeSet = 8.f, kFeMost = 32.f, kUnset = 1e30f;
+constexpr float kLiftW = 6.f, kOverW = 15.f, kUnset = 1e30f;
+constexpr int kExpBias = 127 + 13;               // f_e = 2^(exponent byte - 140): the table holds 2^13 times the grid
 // hardware barriers: the score groups' own (1, 2), both groups' (3); from a group to the value warps: P of a tile is there
 // (4, 5), back: its slot is free (6, 7), a value image is free (8, 9, 10); from group to group: the marks are there (11,
 // 12); from the score to the value warps: a segment's sums (13), back: taken (14).  No warp can meet an earlier or a
@@ -105,9 +109,9 @@ struct Smem {
     uint4 p16[2][R][kTileChunks][32];            // P in f16: [chunk][lane] A fragments
     uint4 pbf[2][R][kTileChunks][32];            // bf16 P
     float fn[2][R][kHeads], fr[2][R][kHeads];    // factors of O before a tile's MMAs (448 dims; RoPE dims)
-    float nm[R][kHeads], gs;                     // the marks
-    float tmax[2][kGroupWarps][R][kHeads], femax[2][kGroupWarps];
-    float lsum[kScoreWarps][R][kHeads], mseg[R][kHeads], ginv;   // a segment's sums, marks and 1 / g
+    float nm[R][kHeads], dm[R][kHeads], er[R][kHeads];   // the marks
+    float tmax[2][kGroupWarps][R][kHeads], wmax[2][kGroupWarps][kFp4 ? R : 1][kHeads];
+    float lsum[kScoreWarps][R][kHeads], mseg[R][kHeads], dseg[R][kHeads];   // a segment's sums and marks
     int32_t chunk_tok[kStages][kTileChunks];     // first token of a tile's chunks; -1: none
     int32_t resc[2];                             // 0: O stays, 1: O *= f, 2: O = 0 (first tile of a segment)
     uint64_t full[kStages], empty[kStages];
@@ -524,8 +528,10 @@ __device__ __forceinline__ void score_role(Smem<kFp4, R>& sm, const Params& P, W
         if (warp == 0) {
             if (lane < kHeads)
 #pragma unroll
-                for (int r = 0; r < R; ++r) sm.nm[r][lane] = kUnset;
-            if (lane == 0) sm.gs = 0.f;   // not set yet
+                for (int r = 0; r < R; ++r) {
+                    sm.nm[r][lane] = kUnset;
+                    sm.dm[r][lane] = sm.er[r][lane] = 0.f;
+                }
         }
         named_barrier(kBarScore, kScoreThreads);
         float c2[R][2];   // logit factors (log2 units) of heads g, g + 8
@@ -563,7 +569,9 @@ __device__ __forceinline__ void score_role(Smem<kFp4, R>& sm, const Params& P, W
             const uint32_t vis = __ballot_sync(0xffffffffu, tok0 >= 0 && tk <= p && (tk > lo || tk < P.sinks)) & 0xFFFFu;
             float acc[R][2][2][4], racc[R][2][4];   // [entries 8 nt ..][half of a step: independent chains]; RoPE part
             uint8_t* img = kFp4 ? sm.img[im] : sm.stage[st];
-            float fe[2][2];   // of the entries mine(nt, i); 0: masked
+            uint32_t eb = 0;   // fp4: the exponent bytes of the entries mine(nt, i), entry 2 nt + i in byte 2 nt + i
+            auto byte_of = [&](int nt, int i) { return (eb >> (8 * (2 * nt + i))) & 0xFFu; };
+            auto seen = [&](int nt, int i) { return ((vis >> mine(nt, i)) & 1) && (!kFp4 || byte_of(nt, i) != 0); };
             if constexpr (kFp4) {
                 const uint8_t* ch = sm.stage[st] + w * kChunk4Bytes;
                 // RoPE rows into the image, eight lanes a row
@@ -585,20 +593,14 @@ __device__ __forceinline__ void score_role(Smem<kFp4, R>& sm, const Params& P, W
                         if (4 * s + c < kSteps && (vis >> (8 * nt + g)) & 1)
                             most = max(most, static_cast<uint32_t>(base - ch[kChunk4Exp + (4 * s + c) * kChunk + 8 * nt + g]));
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const uint32_t eb = ch[kChunk4Exp + kGroups * kChunk + mine(nt, i)];
-                        fe[nt][i] = (vis >> mine(nt, i)) & 1 ? __uint_as_float(eb << 23) * 0x1p-13f : 0.f;
-                    }
+                    for (int i = 0; i < 2; ++i)
+                        eb |= static_cast<uint32_t>(ch[kChunk4Exp + kGroups * kChunk + mine(nt, i)]) << (8 * (2 * nt + i));
                 }
                 if (__any_sync(0xffffffffu, most > static_cast<uint32_t>(kMaxJ))) score_fp4<R, true>(sm, ch, img, w, vis, g, c, lane, acc);
                 else score_fp4<R, false>(sm, ch, img, w, vis, g, c, lane, acc);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.empty[st]);
             } else {
-#pragma unroll
-                for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) fe[nt][i] = (vis >> mine(nt, i)) & 1 ? 1.f : 0.f;
                 if (vis != 0xFFFFu) {   // masked rows are zeroed for the value warps, eight lanes a row (unrolled, the full tiles lose 2 %)
 #pragma unroll 1
                     for (int en = lane >> 3; en < 16; en += 4)
@@ -628,7 +630,17 @@ __device__ __forceinline__ void score_role(Smem<kFp4, R>& sm, const Params& P, W
             }
             // logits x[r][nt][2 k + i]: entry mine(nt, i), head g + 8 k (log2 units), -inf where masked
             float (&x)[R][2][4] = racc;
-            float top[R][2], fmost = fmaxf(fmaxf(fe[0][0], fe[0][1]), fmaxf(fe[1][0], fe[1][1]));
+            float top[R][2];
+            // fp4: f_e and its log2 (of masked entries -inf)
+            auto fe = [&](int nt, int i) { return __uint_as_float(byte_of(nt, i) << 23) * 0x1p-13f; };
+            float lfe[2][2], lmost = -INFINITY;
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    lfe[nt][i] = !kFp4 ? 0.f : seen(nt, i) ? __uint_as_float(0x4B000000u | byte_of(nt, i)) - (0x1p23f + kExpBias) : -INFINITY;
+                    lmost = fmaxf(lmost, lfe[nt][i]);
+                }
 #pragma unroll
             for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -640,49 +652,52 @@ __device__ __forceinline__ void score_role(Smem<kFp4, R>& sm, const Params& P, W
                         for (int i = 0; i < 2; ++i) {
                             const int n = 2 * k + i;
                             const float sum = acc[r][nt][0][n] + acc[r][nt][1][n];
-                            const float v = kFp4 ? fmaf(sum, fe[nt][i], racc[r][nt][n]) : sum + racc[r][nt][n];
-                            x[r][nt][n] = fe[nt][i] > 0.f ? v * c2[r][k] : -INFINITY;
+                            const float v = kFp4 ? fmaf(sum, fe(nt, i), racc[r][nt][n]) : sum + racc[r][nt][n];
+                            x[r][nt][n] = seen(nt, i) ? v * c2[r][k] : -INFINITY;
                             top[r][k] = fmaxf(top[r][k], x[r][nt][n]);
                         }
                 }
             // the marks, as the tile before left them; the slot of P (and of the factors) is free once its last tile is used
             if (T > T0) bar_sync(kBarMark + ((T - 1) & 1), kScoreThreads);
             if (T >= 2) bar_sync(kBarPFree + buf, kHandover);
-            float gs = sm.gs, mk[R][2];
-            bool over = kFp4 && fmost * gs > kFeMost;
+            float mk[R][2], dm[R][2];
+            bool over = false;
 #pragma unroll
             for (int r = 0; r < R; ++r)
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     mk[r][k] = sm.nm[r][g + 8 * k];
+                    dm[r][k] = kFp4 ? sm.dm[r][g + 8 * k] : 0.f;
                     over |= top[r][k] + mk[r][k] > kOver<kFp4>;
+                    if (kFp4) over |= (top[r][k] + mk[r][k]) + (lmost + dm[r][k]) > kOverW;   // at least any w of the lane's
                 }
             int resc = T == T0 ? 2 : 0;
             if (named_barrier_or(kBarGroup + gr, kGroupThreads, over)) {
-                // some weight is too large, or the first tile: the tile's maxima; a head that lies more than 2 above its
-                // mark gets a new one, and the value warps the factors of what they hold
+                // some weight may be too large, or the first tile: the tile's maxima (fp4: of p f_e as well, relative to the warp's
+                // largest p, so that no logit is rounded by adding to it); a head that lies more than 2 above its mark gets a new
+                // one, and the value warps the factors of what they hold
+                float er[R][2];
 #pragma unroll
                 for (int r = 0; r < R; ++r)
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
+                        er[r][k] = kFp4 ? sm.er[r][g + 8 * k] : 0.f;
                         top[r][k] = fmaxf(top[r][k], __shfl_xor_sync(0xffffffffu, top[r][k], 1));
                         top[r][k] = fmaxf(top[r][k], __shfl_xor_sync(0xffffffffu, top[r][k], 2));
                         if (c == 0) sm.tmax[gr][w][r][g + 8 * k] = top[r][k];
+                        if constexpr (kFp4) {
+                            float wt = -INFINITY;
+#pragma unroll
+                            for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                                for (int i = 0; i < 2; ++i)
+                                    if (top[r][k] > -INFINITY) wt = fmaxf(wt, (x[r][nt][2 * k + i] - top[r][k]) + lfe[nt][i]);
+                            wt = fmaxf(wt, __shfl_xor_sync(0xffffffffu, wt, 1));
+                            wt = fmaxf(wt, __shfl_xor_sync(0xffffffffu, wt, 2));
+                            if (c == 0) sm.wmax[gr][w][r][g + 8 * k] = wt;
+                        }
                     }
-                if constexpr (kFp4) {
-                    const uint32_t fm = __reduce_max_sync(0xffffffffu, __float_as_uint(fmost));
-                    if (lane == 0) sm.femax[gr][w] = __uint_as_float(fm);
-                }
                 named_barrier(kBarGroup + gr, kGroupThreads);
-                float fg = 1.f;
-                if constexpr (kFp4) {
-                    const float fm = fmaxf(fmaxf(sm.femax[gr][0], sm.femax[gr][1]), fmaxf(sm.femax[gr][2], sm.femax[gr][3]));
-                    if (fm > 0.f && (gs == 0.f || fm * gs > kFeMost)) {
-                        const float gn = kFeSet / fmaxf(fm, 0x1p-110f);
-                        if (gs != 0.f) fg = gn / gs;
-                        gs = gn;
-                    }
-                }
 #pragma unroll
                 for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -693,15 +708,33 @@ __device__ __forceinline__ void score_role(Smem<kFp4, R>& sm, const Params& P, W
                         const bool first = mk[r][k] == kUnset;
                         const bool set = first ? tm > -INFINITY : tm + mk[r][k] > kLift<kFp4> + 2.f;
                         const float to = set ? kLift<kFp4> - tm : mk[r][k];
-                        const float f = set && !first ? exp2_ftz(to - mk[r][k]) : 1.f;
+                        const float down = set && !first ? to - mk[r][k] : 0.f, f = exp2_ftz(down);
+                        float fw = f;
+                        if constexpr (kFp4) {
+                            const float turn = rintf(down + er[r][k]);
+                            float wt = -INFINITY, d = dm[r][k] - turn;
+                            er[r][k] = (down + er[r][k]) - turn;
+#pragma unroll
+                            for (int i = 0; i < kGroupWarps; ++i)
+                                wt = fmaxf(wt, sm.wmax[gr][i][r][g + 8 * k] + (sm.tmax[gr][i][r][g + 8 * k] + to));
+                            if (first ? set : wt + d > kLiftW + 2.f) {
+                                d = floorf(kLiftW - wt);
+                                er[r][k] = 0.f;
+                            }
+                            fw = first ? 1.f : exp2_ftz(down + (d - dm[r][k]));
+                            dm[r][k] = d;
+                        }
                         mk[r][k] = to;
                         if (w == 0 && c == 0) {
-                            sm.fn[buf][r][g + 8 * k] = f * fg;
+                            sm.fn[buf][r][g + 8 * k] = fw;
                             sm.fr[buf][r][g + 8 * k] = f;
                             sm.nm[r][g + 8 * k] = to;
+                            if (kFp4) {
+                                sm.dm[r][g + 8 * k] = dm[r][k];
+                                sm.er[r][g + 8 * k] = er[r][k];
+                            }
                         }
                     }
-                if (w == 0 && lane == 0) sm.gs = gs;
                 if (T > T0) resc = 1;
             }
             bar_arrive(kBarMark + buf, kScoreThreads);
@@ -717,10 +750,13 @@ __device__ __forceinline__ void score_role(Smem<kFp4, R>& sm, const Params& P, W
                     }
 #pragma unroll
                     for (int nt = 0; nt < 2; ++nt) {
-                        const float p0 = exp2_ftz(x[r][nt][2 * k] + nm[r][k]), p1 = exp2_ftz(x[r][nt][2 * k + 1] + nm[r][k]);
+                        const float y0 = x[r][nt][2 * k] + nm[r][k], y1 = x[r][nt][2 * k + 1] + nm[r][k];
+                        const float p0 = exp2_ftz(y0), p1 = exp2_ftz(y1);
                         l[r][k] += p0 + p1;
                         pb[k][nt] = f32x2_to_bf16x2_bits(p0, p1);
-                        ph[k][nt] = kFp4 ? f32x2_to_f16x2(p0 * (fe[nt][0] * gs), p1 * (fe[nt][1] * gs)) : f32x2_to_f16x2(p0, p1);
+                        // fp4: a second exponential (whole numbers added to y), since p may vanish where p f_e does not
+                        ph[k][nt] = kFp4 ? f32x2_to_f16x2(exp2_ftz(y0 + (lfe[nt][0] + dm[r][k])), exp2_ftz(y1 + (lfe[nt][1] + dm[r][k])))
+                                         : f32x2_to_f16x2(p0, p1);
                     }
                 }
                 sm.p16[buf][r][w][lane] = make_uint4(ph[0][0], ph[1][0], ph[0][1], ph[1][1]);
@@ -745,11 +781,13 @@ __device__ __forceinline__ void score_role(Smem<kFp4, R>& sm, const Params& P, W
                 v += __shfl_xor_sync(0xffffffffu, v, 2);
                 if (c == 0) {
                     sm.lsum[warp][r][g + 8 * k] = v;
-                    if (warp == 0) sm.mseg[r][g + 8 * k] = -mk;
+                    if (warp == 0) {   // dm: stored by this thread itself, or the other group's, which it waited for
+                        sm.mseg[r][g + 8 * k] = -mk;
+                        sm.dseg[r][g + 8 * k] = sm.dm[r][g + 8 * k];
+                    }
                 }
             }
         if (warp == 0 && lane == 0) {
-            sm.ginv = sm.gs != 0.f ? 1.f / sm.gs : 1.f;
             if (wk.t == 0 && wk.len < wk.s.tiles) {   // a cut row begins here: which CTA holds its end
                 const int64_t row = (int64_t)wk.b * P.rows_per_seq + wk.rq;
                 const int64_t end = u1 - wk.left + wk.s.tiles;    // unit behind the row
@@ -874,7 +912,6 @@ __device__ __forceinline__ void value_role(Smem<kFp4, R>& sm, const Params& P, W
         const int j = wk.rq / P.row_groups, h0 = 16 * R * (wk.rq % P.row_groups) + g;
         const int64_t head = ((int64_t)wk.b * P.Q + j) * P.heads + h0;
         const int64_t slot = 2 * (int64_t)blockIdx.x + (wk.t == 0 ? 1 : 0);
-        const float gi = rope ? 1.f : sm.ginv;
         if (__all_sync(0xffffffffu, !*fail)) {
 #pragma unroll
             for (int r = 0; r < R; ++r)
@@ -884,11 +921,14 @@ __device__ __forceinline__ void value_role(Smem<kFp4, R>& sm, const Params& P, W
                     float L = 0.f;
 #pragma unroll
                     for (int i = 0; i < kScoreWarps; ++i) L += sm.lsum[i][r][g + 8 * k];
-                    const float M = sm.mseg[r][g + 8 * k], f = whole ? (L == 0.f ? 0.f : gi / L) : gi;
+                    // 2^-dm in two factors: it may lie below fp32's normal range, and the product not
+                    const int dm = kFp4 && !rope ? static_cast<int>(sm.dseg[r][g + 8 * k]) : 0, half = dm >> 1;
+                    const float M = sm.mseg[r][g + 8 * k], f0 = pow2f(-half), f1 = pow2f(half - dm);
+                    const float f = whole ? (L == 0.f ? 0.f : f1 / L) : f1;
 #pragma unroll
                     for (int q = 0; q < 8; ++q) {
                         const int d = 64 * w + 8 * q + 2 * c;
-                        const float v0 = o[r][q][2 * k] * f, v1 = o[r][q][2 * k + 1] * f;
+                        const float v0 = o[r][q][2 * k] * f0 * f, v1 = o[r][q][2 * k + 1] * f0 * f;
                         if (!whole) *reinterpret_cast<float2*>(P.opart + (slot * R * kHeads + g + h) * kDim + d) = make_float2(v0, v1);
                         else if (h0 + h < P.heads) store_out2(P, (head + h) * kDim + d, v0, v1);
                     }

@@ -458,7 +458,9 @@ CSLD_API csld_status kv_cache_read_paged(const csld_paged_cache* cache, const in
  *   (CSLD_OUT_BF16; then q itself may be out); lse_out [batch][Q][heads] f32 or NULL; 1 <= heads <= CSLD_PAGED_MAX_HEADS,
  *   1 <= Q <= CSLD_MULTI_MAX_Q, 1 <= W, 0 <= sinks; q, out, ws 16-byte aligned.
  * Products: the bf16 query against the stored codes exactly (down to 2^-21 of a head's largest value),
- * softmax weights rounded to f16 (2^-11) for the 8- and 4-bit dims and to bf16 for the RoPE dims; sums and
+ * softmax weights rounded to f16 (2^-11) for the 8- and 4-bit dims and to bf16 for the RoPE dims (fp4: weight
+ * times the entry's scale; small ones to no finer steps than 2^-29 of the head's largest such product, whatever
+ * other entries of less weight look like); sums and
  * statistics in fp32.  A group of an fp4 entry whose scale lies more than 2^26 below the entry's largest
  * counts as zero.  A seq_len below 0 or above max_pages * page_size sets CSLD_DEVERR_SEQ_LEN and counts
  * as 0 or as that.  The order of every sum is fixed by the shapes and lengths: same call, same bits.

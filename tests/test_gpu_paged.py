@@ -735,3 +735,96 @@ def test_window_caches_refuse_what_they_do_not_hold(csld):
     csld.paged_decode_attention(whole, q, SCALE)
     torch.cuda.synchronize()
     assert c.err.item() == 0 and whole.err.item() == 0
+
+
+@pytest.mark.parametrize("heads", [16, 40])
+@pytest.mark.parametrize("k", [10, 14, 18, 22, 28, 40, 100])
+@pytest.mark.parametrize("at", [0, 300, 511])
+def test_fp4_entry_far_larger_than_those_that_carry_weight(csld, heads, k, at):
+    """One token 2^k above the others.  Half of the heads point away from it: its weight is 0 (its logit lies 2^k below) and
+    the result is that of the other tokens, within the bounds formed over those alone.  The other heads see nothing but it."""
+    n, g = 512, synth.gen(k + at)
+    c = Pair(csld, [n], 64, "fp4", seed=47)
+    d = torch.sign(torch.randn(512, generator=g))
+    big = (-d * torch.exp2(torch.randint(0, 3, (512,), generator=g).float()) * 2.0 ** k).to(torch.bfloat16).double().numpy()
+    c.ref.store(0, at, big)
+    c.dev.pages.copy_(torch.from_numpy(c.ref.pages))
+    if heads > 16:
+        _widen(csld, c, LONG)
+    q = 0.5 * torch.randn(1, 1, heads, 512, generator=g) + d
+    q[:, :, 1::2] -= 2 * d
+    q = q.to(torch.bfloat16)
+    o, l = csld.paged_decode_attention(c.dev, q.cuda(), SCALE)
+    vals = c.ref.values(0, range(n))[0]
+    logit = SCALE * (q[0, 0].double().numpy() @ vals.T)
+    rest = np.delete(np.arange(n), at)
+    lead = np.where(np.arange(heads) % 2 == 0, 1.0, -1.0) * (logit[:, rest].max(1) - logit[:, at])
+    assert lead.min() > 200                       # weights below e^-200
+    # the reference over the tokens that have weight: the others' values, as they are stored, or the large one
+    only = R.Cache(np.zeros((n // 64, 64 * R.ENTRY["fp4"]), np.uint8), np.arange(n // 64, dtype=np.int32)[None], np.zeros(1, np.int32), 64, "fp4")
+    for i, t in enumerate(rest):
+        only.store(0, i, vals[t])
+    only.seq_len[0] = n - 1
+    one = R.Cache(np.zeros((1, 64 * R.ENTRY["fp4"]), np.uint8), np.zeros((1, 1), np.int32), np.ones(1, np.int32), 64, "fp4")
+    one.store(0, 0, vals[at])
+    qd = q.double().numpy()
+    R.assert_attention(o[:, :, 0::2], l[:, :, 0::2], R.attention(only, qd[:, :, 0::2], SCALE), f"2^{k} away")
+    R.assert_attention(o[:, :, 1::2], l[:, :, 1::2], R.attention(one, qd[:, :, 1::2], SCALE), f"2^{k} alone")
+
+
+@pytest.mark.parametrize("heads", [16, 24])
+@pytest.mark.parametrize("course", ["any", "falling scales", "rising scales", "weight in the smallest", "weight in the largest"])
+def test_fp4_scales_and_weights_of_any_course(csld, heads, course):
+    """The query meets the RoPE dims alone, so that weights and the scales of the other dims go their own ways: over up to
+    2^60 either, against each other and together, from tile to tile and within one."""
+    n, g = 900, synth.gen(len(course))
+    rng = np.random.default_rng(len(course))
+    t = np.arange(n)
+    logit, e = {"any": (rng.uniform(-40, 0, n), rng.integers(-30, 30, n)),
+                "falling scales": (0.04 * t, np.rint(-0.04 * t / math.log(2))),       # weight times scale stays
+                "rising scales": (-0.04 * t, np.rint(0.04 * t / math.log(2))),
+                "weight in the smallest": (np.where(t % 7 == 3, 0.0, -30.0) + rng.uniform(0, 1, n), np.where(t % 7 == 3, -30, 10)),
+                "weight in the largest": (0.08 * (t // 64 * 64) + rng.uniform(0, 1, n), np.rint(0.05 * t))}[course]
+    c = Pair(csld, [n], 48, "fp4", seed=48)
+    x = torch.randn(n, 512, generator=g).double().numpy()
+    u = np.sign(x[0, 448:])
+    x[:, :448] *= 2.0 ** e[:, None]
+    x[:, 448:] = (logit / (64 * SCALE))[:, None] * u + 0.01 * x[:, 448:]     # a head that holds u has this logit
+    for i in range(n):
+        c.ref.store(0, i, torch.from_numpy(x[i]).to(torch.bfloat16).double().numpy())
+    c.dev.pages.copy_(torch.from_numpy(c.ref.pages))
+    if heads > 16:
+        _widen(csld, c, LONG // 48 * 48)
+    q = torch.zeros(1, 1, heads, 512)
+    q[..., 448:] = torch.from_numpy(u) * torch.tensor([1.0, 0.5, -1.0, 0.125])[torch.arange(heads) % 4][:, None]
+    q = q.to(torch.bfloat16)
+    o, l = csld.paged_decode_attention(c.dev, q.cuda(), SCALE)
+    R.assert_attention(o, l, R.attention(c.ref, q.double().numpy(), SCALE), course)
+
+
+@pytest.mark.parametrize("k", [4, 12, 16, 20, 24, 32])
+def test_fp4_weights_keep_their_bits_beside_a_far_larger_entry(csld, k):
+    """fp32 outputs over 1,024 tokens of one magnitude and weights around 2^-10, the first token 2^k larger and of weight 0: the
+    448 dims within 2^-11 A (f16 weights) and what the logits' rounding moves, for any k."""
+    n, g = 1024, synth.gen(77)
+    x = torch.randn(n, 512, generator=g)
+    d = torch.sign(x[0])
+    x[0] = -d * 2.0 ** k
+    c = Pair(csld, [1], 64, "fp4", seed=49, extra=n)
+    csld.kv_cache_append_paged(c.dev, x[None].to(torch.bfloat16).cuda(), start=torch.zeros(1, dtype=torch.int32, device="cuda"))
+    dev = R.Cache(c.dev.pages.cpu().numpy(), c.ref.table, np.array([n], np.int32), 64, "fp4")
+    q = (0.25 * torch.randn(1, 1, 16, 512, generator=g) + d).to(torch.bfloat16)
+    out = torch.empty(1, 1, 16, 512, device="cuda")
+    csld.paged_decode_attention(c.dev, q.cuda(), SCALE, out=out)
+    v, qd = dev.values(0, range(n))[0], q.double().numpy()[0, 0]
+    s = SCALE * qd @ v.T
+    w = np.exp(s - s.max(1, keepdims=True))
+    w /= w.sum(1, keepdims=True)
+    assert w[:, 0].max() < 2.0 ** -20 / n
+    w[:, 0] = 0.0
+    delta = (512 * 2.0 ** -24 * SCALE * np.abs(qd) @ np.abs(v[1:]).T).max(1)[:, None]
+    ref, A = (w @ v)[:, :448], (w @ np.abs(v))[:, :448]
+    got = out[0, 0].double().cpu().numpy()[:, :448]
+    # 2^-23: the absolute half steps of f16, 2^-30 of the largest weighted entry (weight below 2^-6, values below 6) for each of
+    # 1,024 tokens
+    assert np.all(np.abs(got - ref) <= (2.0 ** -11 + 2 * delta + 2.0 ** -21) * A + 2.0 ** -23)
