@@ -571,7 +571,7 @@ __device__ __forceinline__ void score_role(Smem<kFp4, R>& sm, const Params& P, W
             uint8_t* img = kFp4 ? sm.img[im] : sm.stage[st];
             uint32_t eb = 0;   // fp4: the exponent bytes of the entries mine(nt, i), entry 2 nt + i in byte 2 nt + i
             auto byte_of = [&](int nt, int i) { return (eb >> (8 * (2 * nt + i))) & 0xFFu; };
-            auto seen = [&](int nt, int i) { return ((vis >> mine(nt, i)) & 1) && (!kFp4 || byte_of(nt, i) != 0); };
+            auto seen = [&](int nt, int i) { return (vis >> mine(nt, i)) & 1; };
             if constexpr (kFp4) {
                 const uint8_t* ch = sm.stage[st] + w * kChunk4Bytes;
                 // RoPE rows into the image, eight lanes a row

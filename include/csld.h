@@ -400,6 +400,7 @@ CSLD_API csld_status hybrid_decode_attention_multi(const uint16_t* q, int heads,
  *     3584..3807  [14 groups][16 tokens] e + 127 (255: a group with a NaN)
  *     3808..3823  [16 tokens] the largest of the token's 14 bytes below 255; 3824..3839 zero
  *     3840..5887  [16 tokens][64] bf16 RoPE dims
+ *                   (zero bytes are a token of zeros, as in FP8)
  * -------------------------------------------------------------------------------------- */
 #define CSLD_ENTRY_FP8 8
 #define CSLD_ENTRY_FP4 4

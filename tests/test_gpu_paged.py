@@ -828,3 +828,28 @@ def test_fp4_weights_keep_their_bits_beside_a_far_larger_entry(csld, k):
     # 2^-23: the absolute half steps of f16, 2^-30 of the largest weighted entry (weight below 2^-6, values below 6) for each of
     # 1,024 tokens
     assert np.all(np.abs(got - ref) <= (2.0 ** -11 + 2 * delta + 2.0 ** -21) * A + 2.0 ** -23)
+
+
+@pytest.mark.parametrize("heads", [16, 24])
+@pytest.mark.parametrize("lens,W", [([70], None), ([1, 40], None), ([200, 64], 50)])
+def test_entries_that_were_never_stored_read_and_attend_as_zeros(csld, lens, W, heads):
+    """An fp4 page of zero bytes (as allocate makes it) within a sequence: its tokens are zeros for the read-back and
+    for attention alike, in full and beside stored ones; as in fp8, whose zero bytes are zeros."""
+    for fmt in ("fp8", "fp4"):
+        c = Pair(csld, lens, 16, fmt, seed=50)
+        for b, n in enumerate(lens):
+            for i in range(0, -(-n // 16), 2):                  # every other page
+                c.ref.pages[c.ref.table[b, i]] = 0
+            for t in range(n):
+                if (t // 16) % 2 == 0 and t % 5 == 4:           # and some stored in these
+                    c.ref.store(b, t, _tokens(synth.gen(t), 1)[0].double().numpy())
+        c.dev.pages.copy_(torch.from_numpy(c.ref.pages))
+        if heads > 16 and W is None:
+            _widen(csld, c, LONG)
+        q = torch.randn(len(lens), 1, heads, 512, generator=synth.gen(6)).to(torch.bfloat16)
+        call = (lambda: csld.paged_decode_attention(c.dev, q.cuda(), SCALE)) if W is None else \
+            (lambda: csld.paged_window_attention(c.dev, q.cuda(), W, 3, SCALE))
+        R.assert_attention(*call(), R.attention(c.ref, q.double().numpy(), SCALE, W, 3 if W else 0), f"{fmt} {lens}")
+        back = csld.kv_cache_read_paged(c.dev, torch.zeros(len(lens), dtype=torch.int32, device="cuda"), max(lens))
+        for b, n in enumerate(lens):
+            assert np.array_equal(back[b, :n].double().cpu().numpy(), c.ref.values(b, range(n))[0])
