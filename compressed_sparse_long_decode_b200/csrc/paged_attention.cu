@@ -87,7 +87,7 @@ constexpr int kQSteps = 2 * kSteps + 4;          // 16-dim MMA steps of the quer
 // f16's 11 bits, and no w is off by more than 2^-29 of the largest.
 template <bool kFp4> constexpr float kLift = kFp4 ? 0.f : 5.f;
 template <bool kFp4> constexpr float kOver = kFp4 ? 10.f : 15.f;
-constexpr float kLiftW = 6.f, kOverW = 15.f, kUnset = 1e30f;
+constexpr float kLiftW = 6.f, kOverW = 15.f, kUnset = 3e38f;   // kUnset: above any negative logit's size
 constexpr int kExpBias = 127 + 13;               // f_e = 2^(exponent byte - 140): the table holds 2^13 times the grid
 // hardware barriers: the score groups' own (1, 2), both groups' (3); from a group to the value warps: P of a tile is there
 // (4, 5), back: its slot is free (6, 7), a value image is free (8, 9, 10); from group to group: the marks are there (11,
@@ -543,9 +543,9 @@ __device__ __forceinline__ void score_role(Smem<kFp4, R>& sm, const Params& P, W
                 uint32_t t = 0;
 #pragma unroll
                 for (int i = 0; i < kScoreWarps; ++i) t = max(t, __float_as_uint(sm.tmax[i >> 2][i & 3][r][g + 8 * u]));
-                const int sh = t ? max(-100, min(100, 134 - static_cast<int>(t >> 7))) : 0;
+                const int sh = t ? min(126, 134 - static_cast<int>(t >> 7)) : 0;   // -121 .. 126: 2^sh and 2^-sh are normal numbers
                 sq[u] = pow2f(sh);
-                c2[r][u] = P.scale * 1.4426950408889634f * pow2f(-sh);
+                c2[r][u] = P.scale * (1.4426950408889634f * pow2f(-sh));   // the scale may be tiny where the query is large
             }
             qp.store(sm, r, sq, warp, lane);
         }

@@ -853,3 +853,47 @@ def test_entries_that_were_never_stored_read_and_attend_as_zeros(csld, lens, W, 
         back = csld.kv_cache_read_paged(c.dev, torch.zeros(len(lens), dtype=torch.int32, device="cuda"), max(lens))
         for b, n in enumerate(lens):
             assert np.array_equal(back[b, :n].double().cpu().numpy(), c.ref.values(b, range(n))[0])
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+@pytest.mark.parametrize("heads", [16, 24])
+@pytest.mark.parametrize("e", [-126, -118, -105, -60, 60, 100, 112, 116, 119, 122])
+def test_queries_of_any_magnitude(csld, fmt, heads, e):
+    """Queries 2^e as large under a scale 2^-e as large: the logits are those of e = 0.  Half of the heads 2^-8 of the others."""
+    c = Pair(csld, [300, 20], 64, fmt, seed=51)
+    if heads > 16:
+        _widen(csld, c, LONG)
+    q = torch.randn(2, 1, heads, 512, generator=synth.gen(6)).double()
+    q[:, :, 1::2] *= 2.0 ** -8
+    q = (q * 2.0 ** e).to(torch.bfloat16)
+    scale = float(np.float32(SCALE * 2.0 ** -e))
+    o, l = csld.paged_decode_attention(c.dev, q.cuda(), scale)
+    assert torch.isfinite(q).all() and c.dev.err.item() == 0
+    R.assert_attention(o, l, R.attention(c.ref, q.double().numpy(), scale), f"{fmt} 2^{e}")
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("scale", [2.0 ** 100, -2.0 ** 112])
+def test_logits_near_the_largest_numbers(csld, fmt, scale, wide):
+    """Logits of up to 2^126, all of them negative for some heads: the largest one takes all the weight."""
+    n = 100
+    c = Pair(csld, [n], 32, fmt, seed=52)
+    d = torch.sign(torch.randn(512, generator=synth.gen(8)))
+    size = [1.0 + (37 * t % n) / 64.0 for t in range(n)]     # powers of two and their halves survive both formats
+    for t in range(n):
+        c.ref.store(0, t, (d * 2.0 ** round(size[t])).to(torch.bfloat16).double().numpy())
+    c.ref.store(0, 61, (d * 0.25).double().numpy())          # the smallest and the largest one
+    c.ref.store(0, 12, (d * 16.0).double().numpy())
+    c.dev.pages.copy_(torch.from_numpy(c.ref.pages))
+    if wide:      # the row cut over two CTAs
+        _widen(csld, c, LONG)
+    sign = torch.tensor([1.0, -1.0] * 8)
+    q = (d * sign[:, None])[None, None].to(torch.bfloat16).contiguous()
+    o, l = csld.paged_decode_attention(c.dev, q.cuda(), scale)
+    for h in range(16):
+        up = sign[h].item() * scale > 0
+        val = 16.0 if up else 0.25
+        assert torch.equal(o[0, 0, h].float().cpu(), d * val)
+        want = sign[h].item() * scale * 512 * val
+        assert abs(l[0, 0, h].item() - want) <= 2.0 ** -14 * abs(want)
