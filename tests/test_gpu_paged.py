@@ -897,3 +897,47 @@ def test_logits_near_the_largest_numbers(csld, fmt, scale, wide):
         assert torch.equal(o[0, 0, h].float().cpu(), d * val)
         want = sign[h].item() * scale * 512 * val
         assert abs(l[0, 0, h].item() - want) <= 2.0 ** -14 * abs(want)
+
+
+def _spread(csld, lens, tokens, fmt, seed):
+    """A cache of many sequences, a table for `tokens` of each, pages in random order for the few that hold tokens; and
+    the same in numpy, those sequences alone."""
+    page = 64
+    rng = np.random.default_rng(seed)
+    keep = [b for b, n in enumerate(lens) if n]
+    need = [-(-n // page) for n in lens]
+    order = rng.permutation(sum(need) + 2).astype(np.int32)
+    table = np.full((len(lens), tokens // page), -1, np.int32)
+    at = 0
+    for b in keep:
+        table[b, :need[b]] = order[at:at + need[b]]
+        at += need[b]
+    dev = csld.PagedCache(torch.full((len(order), page * R.ENTRY[fmt]), 0xFF, dtype=torch.uint8, device="cuda"), torch.from_numpy(table).cuda(),
+                          torch.zeros(len(lens), dtype=torch.int32, device="cuda"), page, fmt)
+    x = _tokens(synth.gen(seed), len(keep), max(lens))
+    full = torch.zeros(len(lens), max(lens), 512, dtype=torch.bfloat16, device="cuda")
+    full[keep] = x.cuda()
+    csld.kv_cache_append_paged(dev, full, n_new=torch.tensor(lens, dtype=torch.int32, device="cuda"))
+    torch.cuda.synchronize()
+    assert dev.err.item() == 0
+    return dev, R.Cache(dev.pages.cpu().numpy(), table[keep], np.array([lens[b] for b in keep], np.int32), page, fmt), keep
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+@pytest.mark.parametrize("Q,H,W", [(1, 16, None), (2, 24, None), (1, 16, 1 << 14)])
+def test_more_sequences_than_one_pass_of_the_scan_covers(csld, fmt, Q, H, W):
+    """1,500 sequences with a table for 2,560 tokens each: rows are cut, and which sequence a share begins in comes from three
+    passes of 640; most are empty, long ones lie in every pass and at both ends."""
+    lens = [0] * 1500
+    for b, n in ((0, 1000), (3, 1), (638, 700), (639, 64), (640, 2560), (641, 65), (1279, 130), (1281, 1900), (1498, 17), (1499, 640)):
+        lens[b] = n
+    dev, ref, keep = _spread(csld, lens, 2560, fmt, 61)
+    q = torch.randn(len(lens), Q, H, 512, generator=synth.gen(5)).to(torch.bfloat16)
+    if W is None:
+        o, l = csld.paged_decode_attention(dev, q.cuda(), SCALE)
+    else:
+        o, l = csld.paged_window_attention(dev, q.cuda(), W, 4, SCALE)
+    assert dev.err.item() == 0
+    R.assert_attention(o[keep], l[keep], R.attention(ref, q[keep].double().numpy(), SCALE, W, 4 if W else 0), f"{fmt} {Q} {H} {W}")
+    none = [b for b, n in enumerate(lens) if not n]
+    assert (o[none] == 0).all() and torch.isneginf(l[none]).all()
