@@ -15,6 +15,7 @@
 // lengths load the SMs alike; a CTA walks its share as segments of rows.  A row that lies whole in one share is
 // written out directly; of a row cut by shares each CTA leaves its unnormalised O and (m, l), and
 // paged_merge_kernel joins them.
+// Where windows or capacities are short a CTA takes whole rows instead, without looking at the lengths (launch_paged_attention).
 //
 // Which tensor instructions.  With 16 heads one side of every product is 16 rows.  A tcgen05.mma reads its
 // 128-row operand, here the entries, from shared memory at 128 B a cycle: 45 cycles for 128 x 32 x 32 (measured;
@@ -1212,7 +1213,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid
 
 namespace {
 constexpr int kMaxR = 2;
-constexpr int kMergeTiles = 4;   // what cutting rows costs, in tiles of a CTA's time: the scan of lengths and the merge launch
+constexpr int kMergeTiles = 4;   // what cutting rows costs at the least, in tiles of a CTA's time: the scan of lengths and the merge launch
 constexpr size_t kPartBytes = 2 * kMaxR * kHeads * (kDim * sizeof(float) + sizeof(float2)) + sizeof(int4);   // per CTA
 
 template <bool kFp4, int R>
@@ -1234,6 +1235,7 @@ cudaError_t launch_paged_attention(const PagedView& c, bool fp4, const uint16_t*
     const int64_t t = (chunks + kTileChunks - 1) / kTileChunks;
     // Two 16-head groups a row save decoding once there is work for all SMs: 4 x 64K tokens with 64 heads, 55 tiles a CTA: fp4
     // 171 -> 156 us, fp8 145 -> 126; but 16 windows of 4,096 with 32 heads, 7 tiles: fp4 42 -> 44, fp8 38 -> 42 (14 tiles: even).
+    // Short sequences in a table for long ones take R = 2 too, and lose these few percent.
     const int R = heads > kHeads && (int64_t)c.batch * Q * ((heads + 2 * kHeads - 1) / (2 * kHeads)) * t >= 14 * num_sms ? 2 : 1;
     Params P;
     P.c = c;
@@ -1256,9 +1258,14 @@ cudaError_t launch_paged_attention(const PagedView& c, bool fp4, const uint16_t*
     for (int i = 0; !fp4 && i < 3; ++i)
         if (!make_tensor_map_2d_u8(&maps.rows[i], c.pages, kEntry, (uint64_t)c.n_pages * c.page_size, 128, kChunk << i))
             return cudaErrorInvalidValue;
-    // Whole rows or cut ones.
-    const int64_t rows = (int64_t)c.batch * P.rows_per_seq, n_cta = min64(num_sms, rows);
-    P.whole = (rows + n_cta - 1) / n_cta * t <= rows * t / num_sms + kMergeTiles;
+    // Whole rows a CTA, or rows cut into even shares.  Cutting costs the scan and the merge launch, 9 to 10 us (148 windows of 768
+    // tokens, one row a CTA: fp8 25.2 -> 34.0 us, fp4 26.4 -> 36.0; of 4,096: fp8 95 -> 105; 64 of 128: 11.0 -> 28.4), and pays
+    // where rows do not divide well, or are of unlike lengths, which the host does not know: whole rows are bounded by how far
+    // the longest may exceed the shares.  A window is mostly full, and whole rows stay up to 64 tiles a CTA, where cutting costs
+    // a tenth.  A capacity says little of the lengths: up to 8 tiles, as much again as cutting costs (148 sequences
+    // of up to 128K tokens, log-uniform: whole 2,784 us, cut 722; 37 x 4 queries 2,715 and 911; 140 of up to 4,096: 91.5 and 61.9).
+    const int64_t rows = (int64_t)c.batch * P.rows_per_seq, n_cta = min64(num_sms, rows), per = (rows + n_cta - 1) / n_cta;
+    P.whole = per * t <= rows * t / num_sms + kMergeTiles && per * (t - 1) <= (W > 0 ? 64 : 2 * kMergeTiles);
     cudaError_t e = fp4 ? (R == 2 ? launch_rows<true, 2>(maps, P, P.whole ? n_cta : num_sms, stream)
                                   : launch_rows<true, 1>(maps, P, P.whole ? n_cta : num_sms, stream))
                         : (R == 2 ? launch_rows<false, 2>(maps, P, P.whole ? n_cta : num_sms, stream)

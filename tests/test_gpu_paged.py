@@ -941,3 +941,38 @@ def test_more_sequences_than_one_pass_of_the_scan_covers(csld, fmt, Q, H, W):
     R.assert_attention(o[keep], l[keep], R.attention(ref, q[keep].double().numpy(), SCALE, W, 4 if W else 0), f"{fmt} {Q} {H} {W}")
     none = [b for b, n in enumerate(lens) if not n]
     assert (o[none] == 0).all() and torch.isneginf(l[none]).all()
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+@pytest.mark.parametrize("B,Q", [(148, 1), (37, 4)])
+def test_one_long_sequence_among_as_many_rows_as_sms(csld, fmt, B, Q):
+    """The rows are a multiple of the SMs and one sequence is far longer: right, and not in the time that one CTA takes for it (with
+    even shares it takes little longer than in a batch of one row less)."""
+    n = 64 * 300
+    lens = [1 + 7 * b % 200 for b in range(B)]
+    lens[5] = n
+    dev, ref, keep = _spread(csld, lens, 1 << 16, fmt, 62)
+    q = torch.randn(B, Q, 16, 512, generator=synth.gen(5)).to(torch.bfloat16)
+    o, l = csld.paged_decode_attention(dev, q.cuda(), SCALE)
+    some = [4, 5, 6, B - 1]
+    part = R.Cache(ref.pages, ref.table[some], ref.seq_len[some], 64, fmt)
+    R.assert_attention(o[some], l[some], R.attention(part, q[some].double().numpy(), SCALE), f"{fmt} {B}")
+    less = csld.PagedCache(dev.pages, dev.page_table[:-1].contiguous(), dev.seq_len[:-1].contiguous(), 64, fmt)
+    ws, qd = csld.paged_attention_workspace(), q.cuda()
+    ql = qd[:-1].contiguous()
+
+    def best(f):
+        times = []
+        for _ in range(12):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            for _ in range(4):
+                f()
+            b.record()
+            torch.cuda.synchronize()
+            times.append(a.elapsed_time(b))
+        return min(times)
+
+    whole, fewer = best(lambda: csld.paged_decode_attention(dev, qd, SCALE, ws=ws)), best(lambda: csld.paged_decode_attention(less, ql, SCALE, ws=ws))
+    # even shares: 300 long tiles and about 300 short rows over 148 SMs; one CTA alone: 300 tiles or more in a row
+    assert whole < 2 * fewer, (whole, fewer)
