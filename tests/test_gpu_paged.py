@@ -976,3 +976,53 @@ def test_one_long_sequence_among_as_many_rows_as_sms(csld, fmt, B, Q):
     whole, fewer = best(lambda: csld.paged_decode_attention(dev, qd, SCALE, ws=ws)), best(lambda: csld.paged_decode_attention(less, ql, SCALE, ws=ws))
     # even shares: 300 long tiles and about 300 short rows over 148 SMs; one CTA alone: 300 tiles or more in a row
     assert whole < 2 * fewer, (whole, fewer)
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+def test_window_layers_token_by_token(csld, fmt):
+    """Window layers of a stack over 150 steps through a ring of pages: what lies at every visible token's place is that
+    token (the 448 dims byte for byte, the turned RoPE dims within one bf16 step), and attention matches the
+    reference over the bytes that lie there, within the plain bounds."""
+    B, W, S = 2, 32, 5
+    inp = synth.prefill_inputs(8, seed=0)
+    stack = csld.DecodeStack(B, ["window", "window"], 64, 8, W, 16, inp["bias4"], inp["bias128"], inp["w_idx"], sinks=S,
+                             paged_context=200, paged_fmt=fmt, rope_base=BASE)
+    assert stack.layers[0].ring_tokens is not None
+    g = synth.gen(14)
+    whole = [R.Cache(np.zeros((B * 4, 64 * R.ENTRY[fmt]), np.uint8), np.arange(B * 4, dtype=np.int32).reshape(B, 4), np.zeros(B, np.int32),
+                     64, fmt) for _ in range(2)]
+    none = torch.zeros(2, B, device="cuda"), torch.zeros(2, B, 4, 64, device="cuda"), torch.zeros(2, B, 4, device="cuda")
+    for s in range(150):
+        x, q = _tokens(g, 2, B), torch.randn(2, B, 16, 512, generator=g).to(torch.bfloat16)
+        out, lse = torch.zeros(2, B, 16, 512, device="cuda"), torch.zeros(2, B, 16, device="cuda")
+        stack.step(x.cuda(), none[0], q.cuda(), none[1], none[2], SCALE, out, lse)
+        for i in range(2):
+            whole[i].append(x[i].double().numpy()[:, None], None, None, BASE)
+        if s % 16 != 5 and s not in (0, 63, 64, 128, 149):
+            continue
+        torch.cuda.synchronize()
+        for i, layer in enumerate(stack.layers):
+            dev = R.Cache(layer.pages.cpu().numpy(), layer.page_table.cpu().numpy(), layer.seq_len.cpu().numpy(), 64, fmt)
+            for b in range(B):
+                seen = R.visible(s, W, S)
+                a, want = dev.values(b, seen)[0], whole[i].values(b, seen)[0]
+                assert np.array_equal(a[:, :448], want[:, :448])
+                assert np.all(np.abs(a - want)[:, 448:] <= 2.0 ** -7 * np.abs(want[:, 448:]) + 2.0 ** -20 * 64)
+            R.assert_attention(out[i][:, None], lse[i][:, None], R.attention(dev, q[i].double().numpy()[:, None], SCALE, W, S),
+                               f"{fmt} layer {i} step {s}")
+    assert stack.err.item() == 0
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+@pytest.mark.parametrize("page,n", [(16, 1), (16, 16), (32, 20)])
+def test_a_pool_of_one_page(csld, fmt, page, n):
+    """The smallest pool: fewer rows than the largest copy takes at once."""
+    c = csld.PagedCache.allocate(1, page, page, fmt)
+    assert c.n_pages == 1
+    x, q = _tokens(synth.gen(n), 1, n), torch.randn(1, 1, 16, 512, generator=synth.gen(6)).to(torch.bfloat16)
+    csld.kv_cache_append_paged(c, x.cuda())
+    o, l = csld.paged_decode_attention(c, q.cuda(), SCALE)
+    dev = R.Cache(c.pages.cpu().numpy(), c.page_table.cpu().numpy(), c.seq_len.cpu().numpy(), page, fmt)
+    R.assert_attention(o, l, R.attention(dev, q.double().numpy(), SCALE), f"{fmt} {page}")
+    back = csld.kv_cache_read_paged(c, torch.zeros(1, dtype=torch.int32, device="cuda"), n)
+    assert np.array_equal(back[0].double().cpu().numpy(), dev.values(0, range(n))[0]) and c.err.item() == 0
