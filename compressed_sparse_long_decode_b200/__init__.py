@@ -544,6 +544,7 @@ class PagedCache:
     max_pages, n_pages, ..) and the format cannot be assigned."""
 
     FORMATS = {"fp8": (8, ENTRY_BYTES), "fp4": (4, ENTRY_FP4_BYTES)}
+    _FIXED = ("fmt", "page_size", "entry_bytes", "batch", "max_pages", "n_pages", "device", "ring_tokens", "_struct", "_ref", "_index", "_ring")
 
     def __init__(self, pages, page_table, seq_len, page_size, fmt="fp8", err=None):
         if fmt not in self.FORMATS:
@@ -580,7 +581,7 @@ class PagedCache:
             if _need(value, torch.int32, "err").device != self.device:
                 raise CsldError(f"err is on {value.device}, the cache on {self.device}")
             self.__dict__["err"] = value
-        elif name in self.__dict__:
+        elif name in self._FIXED:
             raise CsldError(f"{name} of a PagedCache cannot be assigned; make another one")
         else:
             super().__setattr__(name, value)

@@ -1026,3 +1026,12 @@ def test_a_pool_of_one_page(csld, fmt, page, n):
     R.assert_attention(o, l, R.attention(dev, q.double().numpy(), SCALE), f"{fmt} {page}")
     back = csld.kv_cache_read_paged(c, torch.zeros(1, dtype=torch.int32, device="cuda"), n)
     assert np.array_equal(back[0].double().cpu().numpy(), dev.values(0, range(n))[0]) and c.err.item() == 0
+
+
+def test_a_cache_takes_a_programs_own_attributes(csld):
+    c = csld.PagedCache.allocate(2, 400, 16, "fp4", window=40, sinks=5)
+    for v in ("layer 0", "layer 1"):
+        c.name = v
+        assert c.name == v
+    with pytest.raises(csld.CsldError):
+        c.ring_tokens = None
