@@ -1233,10 +1233,13 @@ cudaError_t launch_paged_attention(const PagedView& c, bool fp4, const uint16_t*
     int64_t chunks = (c.capacity() + kChunk - 1) / kChunk;
     if (W > 0) chunks = min64(chunks, (min64(sinks, c.capacity()) + kChunk - 1) / kChunk + (min64(W, c.capacity()) + Q - 1 + 2 * kChunk - 2) / kChunk);
     const int64_t t = (chunks + kTileChunks - 1) / kTileChunks;
-    // Two 16-head groups a row save decoding once there is work for all SMs: 4 x 64K tokens with 64 heads, 55 tiles a CTA: fp4
-    // 171 -> 156 us, fp8 145 -> 126; but 16 windows of 4,096 with 32 heads, 7 tiles: fp4 42 -> 44, fp8 38 -> 42 (14 tiles: even).
-    // Short sequences in a table for long ones take R = 2 too, and lose these few percent.
-    const int R = heads > kHeads && (int64_t)c.batch * Q * ((heads + 2 * kHeads - 1) / (2 * kHeads)) * t >= 14 * num_sms ? 2 : 1;
+    // Two 16-head groups a row save decoding where the groups are even in number and there is work for all SMs: 4 x 64K tokens with
+    // 64 heads, 55 tiles a CTA: fp4 175 -> 163 us, fp8 150 -> 127; 16 windows of 6,144 with 64 heads, 21 tiles: fp4 85.2 -> 82.7, fp8
+    // 74.7 -> 69.0; of 4,096, 14 tiles: 66.0 -> 66.7, 58.3 -> 56.8; with 32 heads, 7 tiles: 39.9 -> 44.8, 35.6 -> 38.7.  Of three groups
+    // the second row is half empty: 20 windows of 8,192 with 48 heads, 34 tiles: fp4 99 -> 115, fp8 90 -> 102.  Short sequences in a
+    // table for long ones take R = 2 too, and lose these few percent.
+    const int groups = (heads + kHeads - 1) / kHeads;
+    const int R = groups % 2 == 0 && (int64_t)c.batch * Q * (groups / 2) * t >= 14 * num_sms ? 2 : 1;
     Params P;
     P.c = c;
     P.q = q;

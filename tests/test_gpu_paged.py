@@ -1035,3 +1035,21 @@ def test_a_cache_takes_a_programs_own_attributes(csld):
         assert c.name == v
     with pytest.raises(csld.CsldError):
         c.ring_tokens = None
+
+
+@pytest.mark.parametrize("heads", [24, 32])
+@pytest.mark.parametrize("k", [18, 28, 100])
+@pytest.mark.parametrize("at", [0, 511])
+def test_fp4_entry_far_larger_in_rows_of_two_head_groups(csld, heads, k, at):
+    test_fp4_entry_far_larger_than_those_that_carry_weight(csld, heads, k, at)
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+@pytest.mark.parametrize("heads", [33, 48, 80, 113])
+def test_head_groups_of_either_number_over_a_large_capacity(csld, fmt, heads):
+    """Three, five and eight groups of 16 heads, the last one full or with a single head."""
+    c = Pair(csld, [500, 64], 64, fmt, seed=53)
+    _widen(csld, c, LONG)
+    q = torch.randn(2, 2, heads, 512, generator=synth.gen(heads)).to(torch.bfloat16)
+    o, l = csld.paged_decode_attention(c.dev, q.cuda(), SCALE)
+    R.assert_attention(o, l, R.attention(c.ref, q.double().numpy(), SCALE), f"{fmt} {heads}")
