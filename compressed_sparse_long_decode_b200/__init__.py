@@ -758,7 +758,8 @@ class DecodeStack:
     holds tensors).
 
     kinds: list of "csa" / "hca" / "window" (then: paged_context, the tokens a sequence may reach, and
-    sinks, paged_fmt "fp8" or "fp4", rope_base as for kv_cache_append_paged); csa_cap / hca_cap: compressed-entry capacity per sequence;
+    sinks, paged_fmt "fp8" or "fp4", rope_base as for kv_cache_append_paged; a prompt goes into layers[i] as
+    PagedCache.allocate tells); csa_cap / hca_cap: compressed-entry capacity per sequence;
     pos_bias4 [4], pos_bias128 [128], w_idx [512,64]: the pooling biases and the indexer
     projection (shared by the layers of a kind here; per-layer weights only change bytes)."""
 

@@ -14,7 +14,7 @@ namespace {
 
 constexpr int kAppendWarps = 8;
 
-// Sixteen values as E2M1 codes in the cache's word layout: eight codes from the hardware's paired converts (nearest, ties
+// Eight values as E2M1 codes in the cache's word layout: the codes from the hardware's paired converts (nearest, ties
 // to the even code, saturating), then the signs moved (nibble i's from bit 4i + 3 to the middle of the bytes).
 __device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8]) {
     uint32_t b[4];
@@ -57,7 +57,9 @@ __device__ __forceinline__ AppendSpan append_span(const PagedView& c, int b, int
 
 // One warp per token: lane l < 28 owns dims 16l..16l+15 of the 448, every lane one RoPE pair.  Moves
 // 1024 B in and 576 or 368 B out per token; at one token per sequence (decode) it is a chain of three
-// dependent loads (length, page, token) and bound by their latency.  The RoPE frequencies come in as
+// dependent loads (count, length, page; the token beside the length) and bound by their latency.  Every CTA reads
+// the page table over the sequence's whole new range, all or nothing being stored: as much as the data
+// itself at 800K tokens in pages of 64 (1M fp8 tokens at a time 528 us, eight appends of 128K 437).  The RoPE frequencies come in as
 // kernel parameters and angles are reduced to a fraction of a turn in double, so the sine and cosine
 // are cheap fp32 ones whatever the position.
 // A warp takes kTokens tokens, the CTA's warps in turn; their loads are issued together.

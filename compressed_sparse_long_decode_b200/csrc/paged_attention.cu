@@ -48,10 +48,14 @@
 // Where a query has more than 16 heads and there is work for all SMs a row is two groups of 16 (R = 2): keys are decoded
 // and values loaded once for both.
 //
-// What bounds it (fp4, R = 1, a 64-entry tile, 1M tokens; cycles an SM): HBM 975; f16 MMAs 1,024; ALU (permutes, masks) 1,040;
-// shared memory about 1,700 wavefronts; 6,500 instructions, 1,630 a scheduler; taken: 2,630, 0.6 instructions a cycle
-// and scheduler.  176 us, 2.2 TB/s, 0.34 of the copy rate.  fp8: 84 us for 8 x 64K tokens, 3.6 TB/s, 0.55.
-// A third score group (with four value warps of 128 dims) gave 181 us, more or larger stages nothing.
+// What bounds it (R = 1, a 64-entry tile, 512K tokens; per SM, by ncu's counters): fp4 6,100
+// instructions, 1,520 a scheduler, 1,780 shared-memory wavefronts, 1,024 cycles of f16 MMAs, 975 of HBM; taken: 2,990 cycles, start-up
+// included (1M tokens, merge launch included: 2,670 at the same clock).  No resource is full (issue 0.51, shared memory
+// 0.61, MMAs 0.34): the time goes into latencies and hand-overs between the roles, once per 64 entries, as the stalls at barriers
+// say.  1M tokens: 179 us, 2.16 TB/s, 0.33 of the copy rate.  fp8: 2,540 cycles (issue 0.45, shared memory 0.58, MMAs 0.40);
+// 8 x 64K tokens 85 to 86 us, 3.5 TB/s, 0.54.  Registers spill a little (bytes stored and loaded, fp8 104 and 156, R = 2 252 and
+// 292; fp4 56 and 80, R = 2 216 and 248).
+// A third score group (with four value warps of 128 dims) gave 181 us where two gave 176, more or larger stages nothing.
 // Rows of masked or missing tokens are zeroed before they are used, whatever was in them.  The waits for copies are
 // bounded; one that gives up sets CSLD_DEVERR_TIMEOUT and all roles run out without waiting for copies.
 #include <stdint.h>

@@ -385,7 +385,8 @@ CSLD_API csld_status hybrid_decode_attention_multi(const uint16_t* q, int heads,
  *   seq_len     [batch]  tokens so far (int32, device)
  * page_size: a multiple of 16, 16..1024; pages 16-byte aligned; n_pages * page_size and
  * max_pages * page_size at most 2^31 - 1.  One page may appear in several rows (a shared prefix);
- * appending into such a page is the caller's affair.
+ * appending into such a page is the caller's affair.  A row may also repeat its own pages (a ring behind a sliding
+ * window: later tokens take the places of earlier ones); the tokens of one append must then have places of their own.
  * Formats:
  *   CSLD_ENTRY_FP8  576 B per token, the entry of the other caches (448 E4M3, scale 1, saturating;
  *                   64 bf16), tokens of a page in order.
@@ -395,7 +396,7 @@ CSLD_API csld_status hybrid_decode_attention_multi(const uint16_t* q, int heads,
  *                   NaN), the 64 RoPE dims in bf16.  Kept in chunks of 16 tokens, 5888 B each:
  *     0..3583     [14 groups][16 tokens][16 B] codes; a little-endian 32-bit word holds 8 dims,
  *                 dim i's magnitude index in bits 4i..4i+2, its sign in bit 8i + 7 (i < 4) or
- *                 8(i - 4) + 3: a byte permute then turns half a word into four E4M3 bytes, and the
+ *                 8(i - 4) + 3: a byte permute then turns half a word into four E5M2 bytes, and the
  *                 signs drop in with one masked OR
  *     3584..3807  [14 groups][16 tokens] e + 127 (255: a group with a NaN)
  *     3808..3823  [16 tokens] the largest of the token's 14 bytes below 255; 3824..3839 zero
